@@ -283,6 +283,100 @@ nm_status_t nm_plan_set_split_k(nm_plan_t plan, int32_t splits);
 nm_status_t nm_plan_get_split_k(nm_plan_t plan, int32_t* requested, int32_t* effective);
 nm_status_t nm_spmm_workspace_size(nm_plan_t plan, size_t* bytes);
 
+/* ------------------------------------------------------------------------
+ * Around the product: a layer served with compressed weights. The operators
+ * below follow each other in such a layer: a norm that writes the next
+ * product's 8-bit input, the product (nm_spmm's int32 accumulators for a
+ * prompt, nm_w4_matvec for a few tokens), the gated activation, the product
+ * again. Their plans are host-only objects like nm_plan_t; ownership, errors,
+ * streams and the 16-byte rule are as stated at the top of this file, and
+ * nothing here allocates, synchronises or keeps anything from one call for the
+ * next. They have no backward pass: 8-bit codes and packed weights are not
+ * trained through.
+ * ------------------------------------------------------------------------ */
+
+/* Row operators: each row (token) of x by itself.
+ *  NM_ROWS_RMSNORM: u = x + residual; v = gamma * u; the row's factor is
+ *    f = 1 / sqrt(mean(u^2) + eps); y = v * f.
+ *  NM_ROWS_SWIGLU:  x holds 2 * cols columns, the gate and then the up half;
+ *    v = gate / (1 + exp(-gate)) * up; f = 1; y = v.
+ * x is of type_io (NM_F16 or NM_BF16), or NM_I32: the accumulators of an int8
+ * product, whose value is x * row_scale[row] * col_scale[column].
+ * y is of type_io, or NM_I8: with a = max |v| of the row, y_scale[row] =
+ * a * f / 127 and code = v * (127 / a) rounded to nearest even, so that
+ * code * y_scale is the value; a row of zeros gives codes and scale zero, a
+ * row with a NaN or an infinity a NaN or infinite scale.
+ * Everything is computed in fp32 and rounded once. gamma, residual and h are
+ * of type_io. */
+typedef enum { NM_ROWS_RMSNORM = 0, NM_ROWS_SWIGLU = 1 } nm_rows_op_t;
+typedef struct {
+  int64_t rows, cols;       /* of y; x has 2 * cols columns for NM_ROWS_SWIGLU */
+  int32_t op;               /* nm_rows_op_t */
+  int32_t type_io;          /* NM_F16 or NM_BF16 */
+  int32_t type_x, type_y;   /* type_x: type_io or NM_I32; type_y: type_io or NM_I8 */
+  int64_t ldx, ldr, ldh, ldy; /* rows of x, residual, h, y (ldr and ldh are read for NM_ROWS_RMSNORM only) */
+  float eps;                /* NM_ROWS_RMSNORM: finite and >= 0 */
+} nm_rows_problem_t;
+typedef struct nm_rows_plan* nm_rows_plan_t;
+nm_status_t nm_rows_plan_init(nm_rows_plan_t* plan, const nm_rows_problem_t* problem);
+nm_status_t nm_rows_plan_destroy(nm_rows_plan_t plan);
+
+/* y (and y_scale where y is int8) from x; d_residual may be NULL (none), d_h
+ * may be NULL, else it receives x + residual rounded to type_io (the next
+ * residual); d_h may equal d_residual (ldh == ldr), or dX where x is of
+ * type_io (ldh == ldx). d_row_scale (rows floats) and d_col_scale (columns of
+ * x floats) are given exactly where x is NM_I32, d_y_scale (rows floats)
+ * exactly where y is NM_I8. */
+nm_status_t nm_rmsnorm(nm_rows_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                       const void* d_residual, const void* d_gamma, void* d_h, void* dY, float* d_y_scale,
+                       void* stream);
+nm_status_t nm_swiglu(nm_rows_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                      void* dY, float* d_y_scale, void* stream);
+
+/* Product of n tokens with 4-bit weights:
+ *   y[j][i] = x_scale[j] * sum over groups g of scale[i][g] *
+ *             sum over k in g of (code[i][k] - zero[i][g]) * x[j][k]
+ * W is m x k (out x in features). x is n x k (ldx), y is n x m (ldy), both
+ * row-major (y is nm_spmm's D with order_cd = NM_COL_MAJOR). The kernel is made
+ * for few tokens: up to 48 share one pass over the weights.
+ * x is of type_y, or NM_I8 with one x_scale a token (1 where x is of type_y).
+ * Products of a group are summed in fp32 (exactly in int32 for NM_I8), groups
+ * in fp32, rounded once to type_y. */
+typedef struct {
+  int64_t m, n, k;          /* m <= 2^24, n <= 2^20, k <= 2^20; sparse: k % 4 == 0 */
+  int64_t group;            /* k per scale; 0: one scale a row. Otherwise a multiple of 32 (16-bit x) or 64
+                               (NM_I8), twice that for sparse weights; the last group of a row may be shorter */
+  int32_t type_y;           /* y and the scales: NM_F16 or NM_BF16 */
+  int32_t type_x;           /* type_y or NM_I8 */
+  int32_t sparse;           /* 1: W is 2:4 along k, codes hold the kept values, with nm_compress's metadata */
+  int32_t zeros;            /* 1: a zero point (0..15) a group; 0: the zero point is 8 */
+  int64_t ldx, ldy;
+} nm_w4_problem_t;
+typedef struct nm_w4_plan* nm_w4_plan_t;
+nm_status_t nm_w4_plan_init(nm_w4_plan_t* plan, const nm_w4_problem_t* problem);
+nm_status_t nm_w4_plan_destroy(nm_w4_plan_t plan);
+
+/* Sizes: bytes of the packed weights, scales a row (ceil(k / group), 1 for
+ * group 0), bytes of one row of codes (ceil(kept / 2), kept = k, or k / 2 for
+ * sparse) and of metadata (as nm_compressed_size; 0 for dense). Any output
+ * pointer may be NULL. The packed size depends on neither n nor the strides:
+ * plans that differ in these alone share one packed buffer. */
+nm_status_t nm_w4_sizes(nm_w4_plan_t plan, size_t* packed_bytes, int64_t* groups, int64_t* code_ld,
+                        int64_t* meta_ld);
+
+/* Lay weights out for the kernel, once per weight. d_codes: m rows of code_ld
+ * bytes, two codes a byte, the lower nibble first; d_scales: m x groups of
+ * type_y; d_zeros: m x groups bytes (plans with zeros, else NULL); d_meta: m rows
+ * of meta_ld bytes (sparse plans, else NULL). The inputs are not needed later. */
+nm_status_t nm_w4_pack(nm_w4_plan_t plan, const void* d_codes, const void* d_scales, const void* d_zeros,
+                       const void* d_meta, void* d_packed, void* stream);
+
+/* The product. d_x_scale: n floats, given exactly where x is NM_I8. d_packed
+ * must come from nm_w4_pack with a plan of the same m, k, group, types, sparse
+ * and zeros. */
+nm_status_t nm_w4_matvec(nm_w4_plan_t plan, const void* d_packed, const void* dX, const float* d_x_scale, void* dY,
+                         void* stream);
+
 /* Name of the SpMM kernel the plan dispatches to (static string). */
 const char* nm_plan_kernel_name(nm_plan_t plan);
 

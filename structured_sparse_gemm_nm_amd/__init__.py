@@ -41,6 +41,20 @@ class nm_problem_t(ctypes.Structure):
                 ("order_cd", ctypes.c_int32), ("vector_rows", ctypes.c_int32)]
 
 
+class nm_rows_problem_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("op", ctypes.c_int32),
+                ("type_io", ctypes.c_int32), ("type_x", ctypes.c_int32), ("type_y", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64), ("ldy", ctypes.c_int64),
+                ("eps", ctypes.c_float)]
+
+
+class nm_w4_problem_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("group", ctypes.c_int64),
+                ("type_y", ctypes.c_int32), ("type_x", ctypes.c_int32),
+                ("sparse", ctypes.c_int32), ("zeros", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -79,6 +93,18 @@ def lib():
         L.nm_spmm_noalloc.restype = st; L.nm_spmm_noalloc.argtypes = [P, FP, P, P, P, FP, P, P, P]
         L.nm_spmm_streams.restype = st
         L.nm_spmm_streams.argtypes = [P, FP, P, P, P, FP, P, P, P, ctypes.POINTER(P), I32]
+        L.nm_rows_plan_init.restype = st
+        L.nm_rows_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_rows_problem_t)]
+        L.nm_rows_plan_destroy.restype = st; L.nm_rows_plan_destroy.argtypes = [P]
+        L.nm_rmsnorm.restype = st; L.nm_rmsnorm.argtypes = [P] * 10
+        L.nm_swiglu.restype = st; L.nm_swiglu.argtypes = [P] * 7
+        L.nm_w4_plan_init.restype = st
+        L.nm_w4_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_w4_problem_t)]
+        L.nm_w4_plan_destroy.restype = st; L.nm_w4_plan_destroy.argtypes = [P]
+        L.nm_w4_sizes.restype = st
+        L.nm_w4_sizes.argtypes = [P, ctypes.POINTER(S), ctypes.POINTER(I64), ctypes.POINTER(I64), ctypes.POINTER(I64)]
+        L.nm_w4_pack.restype = st; L.nm_w4_pack.argtypes = [P] * 7
+        L.nm_w4_matvec.restype = st; L.nm_w4_matvec.argtypes = [P] * 6
         L.nm_status_string.restype = ctypes.c_char_p; L.nm_status_string.argtypes = [st]
         L.nm_last_error.restype = ctypes.c_char_p; L.nm_last_error.argtypes = []
         L.nm_version.restype = I32; L.nm_version.argtypes = []
@@ -288,6 +314,203 @@ def nm_dense_gemm(plan, alpha, dA, dB, beta, dC, dD, stream=None):
     a, b = ctypes.c_float(alpha), ctypes.c_float(beta)
     _check(lib().nm_dense_gemm(plan.handle, ctypes.byref(a), _ptr(dA), _ptr(dB), ctypes.byref(b), _ptr(dC), _ptr(dD),
                                _stream(stream)))
+
+
+# ---- the operators around the product: RMS norm, gated SiLU product, few-token product on 4-bit weights ----
+
+NM_ROWS_RMSNORM, NM_ROWS_SWIGLU = 0, 1
+ROWS_OPS = {"rmsnorm": NM_ROWS_RMSNORM, "swiglu": NM_ROWS_SWIGLU}
+_CODES = {"f16": NM_F16, "bf16": NM_BF16, "i8": NM_I8, "i32": NM_I32}
+
+
+def _dtype_code(name):
+    if name not in _CODES:
+        raise ValueError("dtype must be one of %s, got %r" % (sorted(_CODES), name))
+    return _CODES[name]
+
+
+def _address(t, name, dtype, shape, ld, device):
+    """Device address of a tensor after checking it against what the plan says:
+    the kernels read and write the rows it describes. ld: the row stride of a
+    matrix (None for a vector). Raw addresses (int) are the caller's word."""
+    if t is None or type(t) is int:
+        return t
+    if t.get_device() != device:
+        raise ValueError("%s is on %s: every operand must be on the current GPU" % (name, t.device))
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if ld is None:
+        if shape[0] > 1 and t.stride(0) != 1:
+            raise ValueError("%s must be contiguous" % name)
+    else:
+        st = t.stride()
+        if st[0] != ld and shape[0] > 1 and shape[1] > 0 or st[1] != 1 and shape[1] > 1:
+            raise ValueError("%s must have strides %s, got %s" % (name, (ld, 1), st))
+    return t.data_ptr()
+
+
+def _where(t, stream):
+    """(device index, raw stream) of a call whose main operand is t."""
+    if t is None or type(t) is int:
+        device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    else:
+        device = t.get_device()
+        if device < 0:
+            raise ValueError("operands must be GPU tensors, got one on %s" % t.device)
+        if device != torch._C._cuda_getDevice():
+            raise ValueError("operands are on cuda:%d, which is not the current device" % device)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif type(stream) is not int:
+        stream = stream.cuda_stream
+    return device, stream
+
+
+class _LayerPlan:
+    """Owns a plan handle of the operators around the product."""
+
+    _destroy = None
+
+    def __init__(self, handle, problem):
+        self.handle = handle.value
+        self.problem = problem
+
+    def destroy(self):
+        if self.handle is not None:
+            getattr(lib(), self._destroy)(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+class RowsPlan(_LayerPlan):
+    """Plan of nm_rmsnorm or nm_swiglu."""
+
+    _destroy = "nm_rows_plan_destroy"
+
+    def __init__(self, handle, problem, io, x, y):
+        super().__init__(handle, problem)
+        p = problem
+        self.rows, self.cols = p.rows, p.cols
+        self.io_dtype, self.x_dtype, self.y_dtype = TORCH_DTYPES[io], TORCH_DTYPES[x], TORCH_DTYPES[y]
+        self._y = (p.rows, p.cols)
+        self._x = (p.rows, 2 * p.cols if p.op == NM_ROWS_SWIGLU else p.cols)
+        self._strides = (p.ldx, p.ldr, p.ldh, p.ldy)
+
+
+def nm_rows_plan_init(rows, cols, op="rmsnorm", dtype="f16", x_dtype=None, y_dtype=None, ldx=None, ldr=None, ldh=None,
+                      ldy=None, eps=1e-6):
+    """Plan of a row operator (host only). op: "rmsnorm" or "swiglu" (x then has 2 * cols columns). dtype: the
+    16-bit type of residual, gamma and h; x_dtype: dtype, or "i32" for an int8 product's accumulators; y_dtype:
+    dtype, or "i8" with one scale a row."""
+    if op not in ROWS_OPS:
+        raise ValueError("op must be one of %s, got %r" % (sorted(ROWS_OPS), op))
+    x_dtype, y_dtype = x_dtype or dtype, y_dtype or dtype
+    p = nm_rows_problem_t()
+    p.rows, p.cols, p.op, p.eps = rows, cols, ROWS_OPS[op], eps
+    p.type_io, p.type_x, p.type_y = _dtype_code(dtype), _dtype_code(x_dtype), _dtype_code(y_dtype)
+    p.ldx = ldx if ldx is not None else max(1, 2 * cols if op == "swiglu" else cols)
+    p.ldr = ldr if ldr is not None else max(1, cols)
+    p.ldh = ldh if ldh is not None else max(1, cols)
+    p.ldy = ldy if ldy is not None else max(1, cols)
+    h = ctypes.c_void_p()
+    _check(lib().nm_rows_plan_init(ctypes.byref(h), ctypes.byref(p)))
+    return RowsPlan(h, p, dtype, x_dtype, y_dtype)
+
+
+def nm_rmsnorm(plan, dX, d_gamma, dY, y_scale=None, residual=None, h=None, row_scale=None, col_scale=None,
+               stream=None):
+    """y = (x + residual) * gamma / sqrt(mean((x + residual)^2) + eps) by rows; h receives x + residual."""
+    dev, stream = _where(dX, stream)
+    ldx, ldr, ldh, ldy = plan._strides
+    shape, io, f32 = plan._y, plan.io_dtype, torch.float32
+    _check(lib().nm_rmsnorm(
+        plan.handle, _address(dX, "x", plan.x_dtype, plan._x, ldx, dev),
+        _address(row_scale, "row_scale", f32, shape[:1], None, dev),
+        _address(col_scale, "col_scale", f32, shape[1:], None, dev),
+        _address(residual, "residual", io, shape, ldr, dev), _address(d_gamma, "gamma", io, shape[1:], None, dev),
+        _address(h, "h", io, shape, ldh, dev), _address(dY, "y", plan.y_dtype, shape, ldy, dev),
+        _address(y_scale, "y_scale", f32, shape[:1], None, dev), stream))
+
+
+def nm_swiglu(plan, dX, dY, y_scale=None, row_scale=None, col_scale=None, stream=None):
+    """y = silu(gate) * up by rows, gate and up the halves of x's columns."""
+    dev, stream = _where(dX, stream)
+    ldx, _, _, ldy = plan._strides
+    shape, f32 = plan._y, torch.float32
+    _check(lib().nm_swiglu(
+        plan.handle, _address(dX, "x", plan.x_dtype, plan._x, ldx, dev),
+        _address(row_scale, "row_scale", f32, shape[:1], None, dev),
+        _address(col_scale, "col_scale", f32, plan._x[1:], None, dev),
+        _address(dY, "y", plan.y_dtype, shape, ldy, dev),
+        _address(y_scale, "y_scale", f32, shape[:1], None, dev), stream))
+
+
+class W4Plan(_LayerPlan):
+    """Plan of nm_w4_pack and nm_w4_matvec. Attributes mirror the size queries."""
+
+    _destroy = "nm_w4_plan_destroy"
+
+    def __init__(self, handle, problem, y, x):
+        super().__init__(handle, problem)
+        p = problem
+        self.m, self.n, self.k = p.m, p.n, p.k
+        self.y_dtype, self.x_dtype = TORCH_DTYPES[y], TORCH_DTYPES[x]
+        size, groups, code_ld, meta_ld = ctypes.c_size_t(), ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+        _check(lib().nm_w4_sizes(self.handle, ctypes.byref(size), ctypes.byref(groups), ctypes.byref(code_ld),
+                                 ctypes.byref(meta_ld)))
+        self.packed_bytes, self.groups = size.value, groups.value
+        self.code_ld, self.meta_ld = code_ld.value, meta_ld.value
+        self._x, self._y, self._packed = (p.n, p.k), (p.n, p.m), (size.value,)
+        self._strides = (p.ldx, p.ldy)
+
+    def empty_packed(self, device="cuda"):
+        return torch.empty((self.packed_bytes,), dtype=torch.uint8, device=device)
+
+
+def nm_w4_plan_init(m, n, k, group=128, dtype="f16", x_dtype=None, sparse=False, zeros=False, ldx=None, ldy=None):
+    """Plan of y = x W^T for n tokens and W (m x k) in 4 bits (host only). group: k per scale (0: one scale a row);
+    dtype: the 16-bit type of y and the scales; x_dtype: dtype, or "i8" with one scale a token; sparse: W is 2:4."""
+    x_dtype = x_dtype or dtype
+    p = nm_w4_problem_t()
+    p.m, p.n, p.k, p.group = m, n, k, group
+    p.type_y, p.type_x = _dtype_code(dtype), _dtype_code(x_dtype)
+    p.sparse, p.zeros = int(bool(sparse)), int(bool(zeros))
+    p.ldx = ldx if ldx is not None else max(1, k)
+    p.ldy = ldy if ldy is not None else max(1, m)
+    h = ctypes.c_void_p()
+    _check(lib().nm_w4_plan_init(ctypes.byref(h), ctypes.byref(p)))
+    return W4Plan(h, p, dtype, x_dtype)
+
+
+def nm_w4_pack(plan, d_codes, d_scales, d_packed, zeros=None, meta=None, stream=None):
+    """Lay 4-bit weights out for nm_w4_matvec: codes (m x code_ld bytes, two a byte, lower nibble first), scales
+    and zeros (m x groups), meta (m x meta_ld bytes, nm_compress's layout, for 2:4 weights)."""
+    dev, stream = _where(d_packed, stream)
+    m, u8, shape = plan.m, torch.uint8, (plan.m, plan.groups)
+    _check(lib().nm_w4_pack(
+        plan.handle, _address(d_codes, "codes", u8, (m, plan.code_ld), plan.code_ld, dev),
+        _address(d_scales, "scales", plan.y_dtype, shape, plan.groups, dev),
+        _address(zeros, "zeros", u8, shape, plan.groups, dev),
+        _address(meta, "meta", u8, (m, plan.meta_ld), plan.meta_ld, dev),
+        _address(d_packed, "packed", u8, plan._packed, None, dev), stream))
+
+
+def nm_w4_matvec(plan, d_packed, dX, dY, x_scale=None, stream=None):
+    """y (n x m) = x (n x k) times the packed W (m x k) transposed."""
+    dev, stream = _where(dX, stream)
+    ldx, ldy = plan._strides
+    _check(lib().nm_w4_matvec(
+        plan.handle, _address(d_packed, "packed", torch.uint8, plan._packed, None, dev),
+        _address(dX, "x", plan.x_dtype, plan._x, ldx, dev),
+        _address(x_scale, "x_scale", torch.float32, plan._x[:1], None, dev),
+        _address(dY, "y", plan.y_dtype, plan._y, ldy, dev), stream))
 
 
 NM_ALG_AUTO, NM_ALG_TILE128, NM_ALG_TILE256X128, NM_ALG_TILE256, NM_ALG_COUNT = range(5)

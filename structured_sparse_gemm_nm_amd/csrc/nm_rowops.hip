@@ -1,0 +1,396 @@
+// Row operators: the RMS norm with the residual's addition and the gated SiLU
+// product, from 16-bit rows or an int8 product's int32 accumulators, to 16 bits
+// or to 8 bits with one scale a row (formulas in include/nmsparse.h).
+//
+// Both are one pass over memory: a row is read once into registers, its
+// statistics (the sum of squares, the largest magnitude) are reduced over the
+// row's threads, and the row is written. Rows too long for that are read twice,
+// the second time from the caches.
+#include <math.h>
+
+#include <new>
+
+#include "nm_device.h"
+#include "nm_internal.h"
+
+struct nm_rows_plan {
+  nm_rows_problem_t p;
+};
+
+namespace nm {
+
+struct RowArgs {
+  const uint8_t* x;
+  const float* row_scale;
+  const float* col_scale;
+  const uint16_t* residual;
+  const uint16_t* gamma;
+  uint16_t* h;
+  uint8_t* y;
+  float* y_scale;
+  int64_t rows, cols, ldx, ldr, ldh, ldy;
+  float eps, rcols;     // rcols = 1 / cols
+};
+
+constexpr int ROW_V = 8;          // columns a thread takes at a time
+constexpr int ROW_THREADS = 256;
+
+// 16 bytes at an address that may be off the 16-byte grid (the up half of a
+// row starts at any column)
+struct __attribute__((packed, aligned(2))) U16x8 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) U32x4 { u32x4 v; };
+
+// ROW_V columns from column c of a row of `cols`, in fp32; columns past the end are 0.
+template <int IO>
+__device__ __forceinline__ void load16(float (&o)[ROW_V], const uint16_t* row, int64_t c, int64_t cols) {
+  if (c + ROW_V <= cols) {
+    const u32x4 v = ((const U16x8*)(row + c))->v;
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++) o[i] = from_bits16<IO>((uint16_t)(v[i / 2] >> (16 * (i % 2))));
+  } else {
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? from_bits16<IO>(row[c + i]) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void load32(T (&o)[ROW_V], const T* row, int64_t c, int64_t cols) {
+  if (c + ROW_V <= cols) {
+#pragma unroll
+    for (int i = 0; i < ROW_V; i += 4) {
+      const u32x4 v = ((const U32x4*)(row + c + i))->v;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t bits = v[j];   // by itself: a bit cast of v[j] in place reads v[0]
+        o[i + j] = __builtin_bit_cast(T, bits);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? row[c + i] : (T)0;
+  }
+}
+
+// ROW_V values of x at column c of a row: 16-bit, or an accumulator times both scales.
+template <int IO, bool ACC>
+__device__ __forceinline__ void load_x(float (&o)[ROW_V], const RowArgs& A, int64_t row, float rs, int64_t first,
+                                       int64_t c) {
+  if constexpr (ACC) {
+    int32_t a[ROW_V];
+    float cs[ROW_V];
+    load32<int32_t>(a, (const int32_t*)A.x + row * A.ldx + first, c, A.cols);
+    load32<float>(cs, A.col_scale + first, c, A.cols);
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++) o[i] = (float)a[i] * rs * cs[i];
+  } else {
+    load16<IO>(o, (const uint16_t*)A.x + row * A.ldx + first, c, A.cols);
+  }
+}
+
+// silu(g) * u. exp of -|g| neither overflows nor divides by a large number; as
+// the square of exp(-|g| / 2) it keeps the subnormal results that the
+// exponential instruction flushes, which bf16 rows can hold.
+__device__ __forceinline__ float gated(float g, float u) {
+  const float half = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * 0.72134752044448f), e = half * half;
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  return g * (g < 0.0f ? e * r : r) * u;
+}
+
+template <int IO>
+__device__ __forceinline__ void store16(uint16_t* row, int64_t c, int64_t cols, const float (&v)[ROW_V]) {
+  uint16_t o[ROW_V];
+#pragma unroll
+  for (int i = 0; i < ROW_V; i++) o[i] = to_bits16<IO>(v[i]);
+  if (c + ROW_V <= cols) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[i] = (uint32_t)o[2 * i] | (uint32_t)o[2 * i + 1] << 16;
+    *(u32x4*)(row + c) = w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++)
+      if (c + i < cols) row[c + i] = o[i];
+  }
+}
+
+// round(v * r) in 8 bits; r = 127 / (largest magnitude) may be infinite (a row
+// of zeros or of the smallest values): NaN converts to 0, the rest is clamped.
+__device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, const float (&v)[ROW_V], float r) {
+  uint32_t o[ROW_V];
+#pragma unroll
+  for (int i = 0; i < ROW_V; i++) {
+    const float t = __builtin_rintf(v[i] * r);
+    o[i] = t != t ? 0u : (uint32_t)(int)__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) & 0xFFu;
+  }
+  if (c + ROW_V <= cols) {
+    *(u32x2*)(row + c) = u32x2{o[0] | o[1] << 8 | o[2] << 16 | o[3] << 24, o[4] | o[5] << 8 | o[6] << 16 | o[7] << 24};
+  } else {
+#pragma unroll
+    for (int i = 0; i < ROW_V; i++)
+      if (c + i < cols) row[c + i] = (uint8_t)o[i];
+  }
+}
+
+// Sum and largest magnitude over the block. Magnitudes are compared as the bits
+// of |v|, which order as the values do and put a NaN above infinity, so that it
+// reaches the scale.
+__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
+  __shared__ float ps[16];
+  __shared__ uint32_t pt[16];
+  for (int o = 32; o > 0; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  }
+  const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) { ps[w] = sum; pt[w] = top; }
+  __syncthreads();
+  sum = 0.0f;
+  for (int i = 0; i < n; i++) { sum += ps[i]; top = max(top, pt[i]); }
+}
+
+// One block a row. C > 0: the row sits in C pieces of ROW_V columns a thread;
+// C = 0: any length, read twice.
+template <int OP, int IO, bool ACC, bool Y8, int C>
+__global__ void __launch_bounds__(ROW_THREADS) row_op_kernel(RowArgs A) {
+  const int64_t row = blockIdx.x;
+  const float rs = ACC ? A.row_scale[row] : 1.0f;
+
+  // v before the row's factor; the norm's u goes to h and into the sum
+  auto make = [&](float (&v)[ROW_V], int64_t c, float& sum, bool write_h) {
+    load_x<IO, ACC>(v, A, row, rs, 0, c);
+    if constexpr (OP == NM_ROWS_RMSNORM) {
+      float g[ROW_V];
+      if (A.residual) {
+        float r[ROW_V];
+        load16<IO>(r, A.residual + row * A.ldr, c, A.cols);
+#pragma unroll
+        for (int i = 0; i < ROW_V; i++) v[i] += r[i];
+      }
+      if (write_h && A.h) store16<IO>(A.h + row * A.ldh, c, A.cols, v);
+      load16<IO>(g, A.gamma, c, A.cols);
+#pragma unroll
+      for (int i = 0; i < ROW_V; i++) {
+        sum = __builtin_fmaf(v[i], v[i], sum);
+        v[i] *= g[i];
+      }
+    } else {
+      float u[ROW_V];
+      load_x<IO, ACC>(u, A, row, rs, A.cols, c);
+#pragma unroll
+      for (int i = 0; i < ROW_V; i++) v[i] = gated(v[i], u[i]);
+    }
+  };
+  auto largest = [&](const float (&v)[ROW_V], uint32_t& top) {
+    if constexpr (Y8) {
+#pragma unroll
+      for (int i = 0; i < ROW_V; i++) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+    }
+  };
+
+  float sum = 0.0f;
+  uint32_t top = 0;
+  float v[C > 0 ? C : 1][ROW_V];
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int p = 0; p < C; p++) {
+      const int64_t c = (int64_t)(p * ROW_THREADS + threadIdx.x) * ROW_V;
+      if (c < A.cols) {
+        make(v[p], c, sum, true);
+        largest(v[p], top);
+      }
+    }
+  } else {
+    for (int64_t c = (int64_t)threadIdx.x * ROW_V; c < A.cols; c += ROW_THREADS * ROW_V) {
+      make(v[0], c, sum, false);
+      largest(v[0], top);
+    }
+  }
+  float f = 1.0f, r = 0.0f;
+  if constexpr (OP == NM_ROWS_RMSNORM || Y8) row_reduce(sum, top);
+  if constexpr (OP == NM_ROWS_RMSNORM) f = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, A.rcols, A.eps));
+  if constexpr (Y8) {
+    const float a = __builtin_bit_cast(float, top);
+    r = 127.0f / a;
+    if (threadIdx.x == 0) A.y_scale[row] = a * f / 127.0f;
+  }
+  auto write = [&](float (&w)[ROW_V], int64_t c) {
+    if constexpr (Y8) {
+      store8(A.y + row * A.ldy, c, A.cols, w, r);
+    } else {
+#pragma unroll
+      for (int i = 0; i < ROW_V; i++) w[i] *= f;
+      store16<IO>((uint16_t*)A.y + row * A.ldy, c, A.cols, w);
+    }
+  };
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int p = 0; p < C; p++) {
+      const int64_t c = (int64_t)(p * ROW_THREADS + threadIdx.x) * ROW_V;
+      if (c < A.cols) write(v[p], c);
+    }
+  } else {
+    for (int64_t c = (int64_t)threadIdx.x * ROW_V; c < A.cols; c += ROW_THREADS * ROW_V) {
+      float unused = 0.0f;
+      make(v[0], c, unused, true);
+      write(v[0], c);
+    }
+  }
+}
+
+template <int OP, int IO, bool ACC, bool Y8, int C>
+hipError_t row_go(const RowArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C>), dim3((unsigned)a.rows), dim3(ROW_THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int OP, int IO, bool ACC, bool Y8>
+hipError_t row_len(const RowArgs& a, hipStream_t s) {
+  const int64_t per = ROW_THREADS * ROW_V;
+  if (a.cols <= per) return row_go<OP, IO, ACC, Y8, 1>(a, s);
+  if (a.cols <= 2 * per) return row_go<OP, IO, ACC, Y8, 2>(a, s);
+  if (a.cols <= 4 * per) return row_go<OP, IO, ACC, Y8, 4>(a, s);
+  if (a.cols <= 8 * per) return row_go<OP, IO, ACC, Y8, 8>(a, s);
+  return row_go<OP, IO, ACC, Y8, 0>(a, s);
+}
+
+template <int OP, int IO>
+hipError_t row_types(const nm_rows_problem_t& p, const RowArgs& a, hipStream_t s) {
+  const bool y8 = p.type_y == NM_I8;
+  if (p.type_x == NM_I32) return y8 ? row_len<OP, IO, true, true>(a, s) : row_len<OP, IO, true, false>(a, s);
+  return y8 ? row_len<OP, IO, false, true>(a, s) : row_len<OP, IO, false, false>(a, s);
+}
+
+static nm_status_t row_fail(nm_status_t st, const char* msg) {
+  try {
+    set_error(msg);
+  } catch (...) {   // no memory for the message: the status still tells
+  }
+  return st;
+}
+
+static bool row_aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// What nm_rmsnorm and nm_swiglu check alike; NM_OK with go = false: nothing to do.
+static nm_status_t row_check(nm_rows_plan_t plan, int op, const void* dX, const float* d_row_scale,
+                             const float* d_col_scale, const void* dY, const float* d_y_scale, bool& go) {
+  go = false;
+  if (!plan) return row_fail(NM_ERR_INVALID_ARG, "plan is NULL");
+  const nm_rows_problem_t& p = plan->p;
+  if (p.op != op) return row_fail(NM_ERR_INVALID_ARG, "the plan is for the other row operator");
+  const bool empty = p.rows == 0 || p.cols == 0, acc = p.type_x == NM_I32, y8 = p.type_y == NM_I8;
+  if (!row_aligned(dX) || !row_aligned(d_row_scale) || !row_aligned(d_col_scale) || !row_aligned(dY) ||
+      !row_aligned(d_y_scale))
+    return row_fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  if (empty) return NM_OK;
+  if (!dX || !dY) return row_fail(NM_ERR_INVALID_ARG, "dX / dY is NULL");
+  if ((d_row_scale != nullptr) != acc || (d_col_scale != nullptr) != acc)
+    return row_fail(NM_ERR_INVALID_ARG, "d_row_scale and d_col_scale must be given exactly where x is int32");
+  if ((d_y_scale != nullptr) != y8)
+    return row_fail(NM_ERR_INVALID_ARG, "d_y_scale must be given exactly where y is int8");
+  go = true;
+  return NM_OK;
+}
+
+static RowArgs row_args(const nm_rows_problem_t& p, const void* dX, const float* d_row_scale,
+                        const float* d_col_scale, void* dY, float* d_y_scale) {
+  RowArgs a = {};
+  a.x = (const uint8_t*)dX;
+  a.row_scale = d_row_scale;
+  a.col_scale = d_col_scale;
+  a.y = (uint8_t*)dY;
+  a.y_scale = d_y_scale;
+  a.rows = p.rows;
+  a.cols = p.cols;
+  a.ldx = p.ldx;
+  a.ldr = p.ldr;
+  a.ldh = p.ldh;
+  a.ldy = p.ldy;
+  a.eps = p.eps;
+  a.rcols = (float)(1.0 / (double)p.cols);
+  return a;
+}
+
+static nm_status_t row_hip(hipError_t e) {
+  return e == hipSuccess ? NM_OK : row_fail(NM_ERR_HIP, hipGetErrorString(e));
+}
+
+}  // namespace nm
+
+using namespace nm;
+
+extern "C" {
+
+nm_status_t nm_rows_plan_init(nm_rows_plan_t* plan, const nm_rows_problem_t* p) {
+  if (!plan) return row_fail(NM_ERR_INVALID_ARG, "plan is NULL");
+  *plan = nullptr;
+  if (!p) return row_fail(NM_ERR_INVALID_ARG, "problem is NULL");
+  if (p->op != NM_ROWS_RMSNORM && p->op != NM_ROWS_SWIGLU)
+    return row_fail(NM_ERR_INVALID_ARG, "op must be NM_ROWS_RMSNORM or NM_ROWS_SWIGLU");
+  if (p->type_io != NM_F16 && p->type_io != NM_BF16)
+    return row_fail(NM_ERR_INVALID_ARG, "type_io must be NM_F16 or NM_BF16");
+  if (p->type_x != p->type_io && p->type_x != NM_I32)
+    return row_fail(NM_ERR_INVALID_ARG, "type_x must be type_io or NM_I32");
+  if (p->type_y != p->type_io && p->type_y != NM_I8)
+    return row_fail(NM_ERR_INVALID_ARG, "type_y must be type_io or NM_I8");
+  const bool norm = p->op == NM_ROWS_RMSNORM;
+  if (norm && !(isfinite(p->eps) && p->eps >= 0.0f))
+    return row_fail(NM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (p->rows < 0 || p->cols < 0) return row_fail(NM_ERR_SHAPE, "rows and cols must be >= 0");
+  // the grid: one block of 256 threads a row, under 2^32 threads
+  if (p->rows >= ((int64_t)1 << 24) || p->cols > ((int64_t)1 << 30))
+    return row_fail(NM_ERR_SHAPE, "rows must be < 2^24 and cols <= 2^30");
+  const int64_t limit = (int64_t)1 << 46, width = norm ? p->cols : 2 * p->cols;
+  struct { int64_t ld, len; int es; } lines[4] = {{p->ldx, width, p->type_x == NM_I32 ? 4 : 2},
+                                                  {p->ldy, p->cols, p->type_y == NM_I8 ? 1 : 2},
+                                                  {p->ldr, p->cols, 2},
+                                                  {p->ldh, p->cols, 2}};
+  for (int i = 0; i < (norm ? 4 : 2); i++) {
+    if (lines[i].ld < (lines[i].len > 0 ? lines[i].len : 1))
+      return row_fail(NM_ERR_SHAPE, "leading dimension smaller than the row length");
+    if (lines[i].ld > limit || (double)p->rows * (double)lines[i].ld > (double)limit)
+      return row_fail(NM_ERR_SHAPE, "matrix too large");
+    if (lines[i].len * lines[i].es >= 16 && lines[i].ld * lines[i].es % 16 != 0)
+      return row_fail(NM_ERR_ALIGN, "rows of 16 bytes or more must start on 16-byte boundaries (ld * elem size % 16)");
+  }
+  nm_rows_plan* pl = new (std::nothrow) nm_rows_plan();
+  if (!pl) return row_fail(NM_ERR_INVALID_ARG, "out of host memory");
+  pl->p = *p;
+  *plan = pl;
+  return row_fail(NM_OK, "");
+}
+
+nm_status_t nm_rows_plan_destroy(nm_rows_plan_t plan) {
+  delete plan;
+  return NM_OK;
+}
+
+nm_status_t nm_rmsnorm(nm_rows_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                       const void* d_residual, const void* d_gamma, void* d_h, void* dY, float* d_y_scale,
+                       void* stream) {
+  bool go;
+  const nm_status_t st = row_check(plan, NM_ROWS_RMSNORM, dX, d_row_scale, d_col_scale, dY, d_y_scale, go);
+  if (st != NM_OK) return st;
+  if (!row_aligned(d_residual) || !row_aligned(d_gamma) || !row_aligned(d_h))
+    return row_fail(NM_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  if (!go) return NM_OK;
+  if (!d_gamma) return row_fail(NM_ERR_INVALID_ARG, "d_gamma is NULL");
+  RowArgs a = row_args(plan->p, dX, d_row_scale, d_col_scale, dY, d_y_scale);
+  a.residual = (const uint16_t*)d_residual;
+  a.gamma = (const uint16_t*)d_gamma;
+  a.h = (uint16_t*)d_h;
+  hipStream_t s = (hipStream_t)stream;
+  return row_hip(plan->p.type_io == NM_F16 ? row_types<NM_ROWS_RMSNORM, DT_F16>(plan->p, a, s)
+                                           : row_types<NM_ROWS_RMSNORM, DT_BF16>(plan->p, a, s));
+}
+
+nm_status_t nm_swiglu(nm_rows_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                      void* dY, float* d_y_scale, void* stream) {
+  bool go;
+  const nm_status_t st = row_check(plan, NM_ROWS_SWIGLU, dX, d_row_scale, d_col_scale, dY, d_y_scale, go);
+  if (st != NM_OK || !go) return st;
+  const RowArgs a = row_args(plan->p, dX, d_row_scale, d_col_scale, dY, d_y_scale);
+  hipStream_t s = (hipStream_t)stream;
+  return row_hip(plan->p.type_io == NM_F16 ? row_types<NM_ROWS_SWIGLU, DT_F16>(plan->p, a, s)
+                                           : row_types<NM_ROWS_SWIGLU, DT_BF16>(plan->p, a, s));
+}
+
+}  // extern "C"
