@@ -20,7 +20,7 @@ CAL_LIB = os.path.join(HERE, "libnmcal.so")       # calibration loops for the be
 SOURCES = ["nm_api.hip", "nm_prune.hip", "nm_rows.hip", "nm_vw.hip", "nm_gemm.hip", "nm_gemm_f16.hip", "nm_gemm_bf16.hip",
            "nm_gemm_i8.hip",
            "nm_skinny_f16.hip", "nm_skinny_bf16.hip", "nm_skinny_i8.hip",
-           "nm_rowops.hip", "nm_w4.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip", "nm_w4_i8.hip"]
+           "nm_rowops.hip", "nm_w4.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip", "nm_w4_i8.hip", "nm_w4_i8_bf16.hip"]
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 CLANG = os.path.join(ROCM, "llvm", "bin", "clang++")
@@ -81,15 +81,53 @@ def _m0_check():
     return out
 
 
+# A sparse matrix instruction whose result registers overlap the ones it reads
+# as A or B takes an operand that the accumulator's initial value has already
+# overwritten. The compiler has formed such instructions where the two halves
+# of B met in a loop variable; the units that hold sparse instructions are
+# compiled with their assembly kept, and one such instruction fails the build.
+SPARSE_SOURCES = ("nm_gemm_f16.hip", "nm_gemm_bf16.hip", "nm_gemm_i8.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip",
+                  "nm_w4_i8.hip", "nm_w4_i8_bf16.hip")
+
+
+def check_sparse_operands(asm_path):
+    """Sparse matrix instructions whose result overlaps the A or B registers (empty list: sound)."""
+    import re
+    bad = []
+
+    def regs(t):
+        m = re.match(r"([av])\[(\d+):(\d+)\]$", t)
+        return (m.group(1), int(m.group(2)), int(m.group(3))) if m else None
+
+    def meet(x, y):
+        return x is not None and y is not None and x[0] == y[0] and x[1] <= y[2] and y[1] <= x[2]
+
+    for line in open(asm_path):
+        t = line.split(";")[0].strip()
+        if not t.startswith("v_smfmac"):
+            continue
+        d, a, b = (regs(x.strip()) for x in t.split(None, 1)[1].split(",")[:3])
+        if d is None or a is None or b is None or meet(d, a) or meet(d, b):
+            bad.append(t)
+    return bad
+
+
 def _compile(src):
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    stem = os.path.splitext(src)[0]
+    obj = os.path.join(BUILD, stem + ".o")
     cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    if src in SPARSE_SOURCES:
+        cmd += ["-save-temps=obj"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l)
     if r.returncode != 0:
         raise RuntimeError("compile failed: %s\n%s" % (" ".join(cmd), msgs))
     if msgs.strip():
         sys.stderr.write(msgs + "\n")
+    if src in SPARSE_SOURCES:
+        bad = check_sparse_operands(os.path.join(BUILD, "%s-hip-amdgcn-amd-amdhsa-%s.s" % (stem, ARCH)))
+        if bad:
+            raise RuntimeError("%s: sparse matrix instructions overwrite their operands: %s" % (src, "; ".join(bad[:5])))
     return obj
 
 

@@ -32,19 +32,18 @@ struct W4Args {
   uint16_t* y;
   int64_t ldx, ldy;
   int32_t m, n, k;
-  int32_t tiles, groups;
-  uint32_t group_magic;  // group of scale application u: umulhi(u, group_magic), or u itself where this is 0
-  int32_t y_bf16;
+  int32_t row_tiles, tiles, groups;
+  uint32_t group_magic;  // group of scale application u: umulhi(2 u, group_magic)
 };
 
 struct W4Shape {
   bool sparse, zeros;
   int flushes;
-  int64_t row_tiles;
 };
 
 hipError_t launch_w4_f16(const W4Args& a, const W4Shape& sh, hipStream_t s);
 hipError_t launch_w4_bf16(const W4Args& a, const W4Shape& sh, hipStream_t s);
-hipError_t launch_w4_i8(const W4Args& a, const W4Shape& sh, hipStream_t s);
+hipError_t launch_w4_i8_f16(const W4Args& a, const W4Shape& sh, hipStream_t s);
+hipError_t launch_w4_i8_bf16(const W4Args& a, const W4Shape& sh, hipStream_t s);
 
 }  // namespace nm

@@ -54,9 +54,8 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs A) {
       }
       int nib;   // nibble that holds code i (the orders the kernels unpack, nm_w4_kernels.h)
       if (A.x_type == NM_F16) nib = (i >> 1) + 4 * (i & 1);
-      else if (A.x_type == NM_I8) nib = i < 4 ? 2 * i : 2 * (i - 4) + 1;
-      else nib = i;
-      if (A.x_type == NM_I8 && !A.zeros) c ^= 8u;
+      else nib = i < 4 ? 2 * i : 2 * (i - 4) + 1;
+      if (A.x_type != NM_F16 && !A.zeros) c ^= 8u;
       w |= c << (4 * nib);
     }
     ((uint32_t*)(A.out_codes + b * 1024))[threadIdx.x] = w;
@@ -129,12 +128,12 @@ nm_status_t nm_w4_plan_init(nm_w4_plan_t* plan, const nm_w4_problem_t* p) {
   pl->groups = p->group == 0 || p->group >= p->k ? 1 : (p->k + p->group - 1) / p->group;
   const int steps = (int)(tile_k / step);   // 4 (16-bit x) or 2 (8-bit x)
   pl->flushes = 1;
-  pl->group_magic = 1;                      // one group a row: every application is group 0
+  pl->group_magic = 0;                      // one group a row: every application is group 0
   if (pl->groups > 1) {
     while (p->group % (tile_k / pl->flushes) != 0 && pl->flushes < steps) pl->flushes *= 2;
     // u < 2^15 applications, at most 2^15 a group: the rounded-up reciprocal divides exactly
     const uint64_t per = (uint64_t)(p->group / (tile_k / pl->flushes));
-    pl->group_magic = per == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + per - 1) / per);
+    pl->group_magic = (uint32_t)((((uint64_t)1 << 31) + per - 1) / per);
   }
   pl->code_ld = (kept + 1) / 2;
   pl->meta_ld = ((kept + 3) / 4 + 15) / 16 * 16;
@@ -229,15 +228,16 @@ nm_status_t nm_w4_matvec(nm_w4_plan_t plan, const void* d_packed, const void* dX
   a.m = (int32_t)p.m;
   a.n = (int32_t)p.n;
   a.k = (int32_t)p.k;
+  a.row_tiles = (int32_t)plan->row_tiles;
   a.tiles = (int32_t)plan->tiles;
   a.groups = (int32_t)plan->groups;
   a.group_magic = plan->group_magic;
-  a.y_bf16 = p.type_y == NM_BF16;
-  const W4Shape sh = {p.sparse != 0, p.zeros != 0, plan->flushes, plan->row_tiles};
+  const W4Shape sh = {p.sparse != 0, p.zeros != 0, plan->flushes};
   hipStream_t s = (hipStream_t)stream;
   if (p.type_x == NM_F16) return w4_hip(launch_w4_f16(a, sh, s));
   if (p.type_x == NM_BF16) return w4_hip(launch_w4_bf16(a, sh, s));
-  return w4_hip(launch_w4_i8(a, sh, s));
+  if (p.type_y == NM_F16) return w4_hip(launch_w4_i8_f16(a, sh, s));
+  return w4_hip(launch_w4_i8_bf16(a, sh, s));
 }
 
 }  // extern "C"

@@ -3,6 +3,6 @@
 
 namespace nm {
 
-hipError_t launch_w4_bf16(const W4Args& a, const W4Shape& sh, hipStream_t s) { return w4_dispatch<DT_BF16>(a, sh, s); }
+hipError_t launch_w4_bf16(const W4Args& a, const W4Shape& sh, hipStream_t s) { return w4_dispatch<DT_BF16, true>(a, sh, s); }
 
 }  // namespace nm

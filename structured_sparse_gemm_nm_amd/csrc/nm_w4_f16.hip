@@ -3,6 +3,6 @@
 
 namespace nm {
 
-hipError_t launch_w4_f16(const W4Args& a, const W4Shape& sh, hipStream_t s) { return w4_dispatch<DT_F16>(a, sh, s); }
+hipError_t launch_w4_f16(const W4Args& a, const W4Shape& sh, hipStream_t s) { return w4_dispatch<DT_F16, false>(a, sh, s); }
 
 }  // namespace nm
