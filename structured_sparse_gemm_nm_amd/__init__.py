@@ -55,17 +55,22 @@ class nm_w4_problem_t(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
-_lib = None
+_lib = _calls = None
 
 
 def lib():
-    """Load libnmsparse.so; raises if it has not been built."""
-    global _lib
+    """Load libnmsparse.so and its call extension; raises if they have not been built."""
+    global _lib, _calls
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libnmsparse.so is not built (run __graft_entry__.build() or "
                                "python structured_sparse_gemm_nm_amd/build.py); no fallback exists")
         L = ctypes.CDLL(LIB_PATH)
+        try:
+            from . import _nmcall
+        except ImportError as e:
+            raise RuntimeError("_nmcall.so is not built for this torch (run __graft_entry__.build()): %s" % e)
+        _calls = _nmcall
         P, I32, I64, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         st = ctypes.c_int
         L.nm_plan_init.restype = st; L.nm_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_problem_t)]
@@ -372,12 +377,19 @@ class _LayerPlan:
     """Owns a plan handle of the operators around the product."""
 
     _destroy = None
+    _norm_call = _gate_call = _product_call = None
 
     def __init__(self, handle, problem):
         self.handle = handle.value
         self.problem = problem
 
+    def _call(self, name, main, *specs):
+        """The entry point with the operands it takes, in its order; main: the operand whose device counts."""
+        fn = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+        return _calls.Call(fn, self.handle, main, specs)
+
     def destroy(self):
+        self._norm_call = self._gate_call = self._product_call = None
         if self.handle is not None:
             getattr(lib(), self._destroy)(self.handle)
             self.handle = None
@@ -402,6 +414,14 @@ class RowsPlan(_LayerPlan):
         self._y = (p.rows, p.cols)
         self._x = (p.rows, 2 * p.cols if p.op == NM_ROWS_SWIGLU else p.cols)
         self._strides = (p.ldx, p.ldr, p.ldh, p.ldy)
+        f32, io, rows = torch.float32, self.io_dtype, self._y[:1]
+        x_specs = (self.x_dtype, self._x, p.ldx), (f32, rows, None), (f32, self._x[1:], None)
+        y_specs = (self.y_dtype, self._y, p.ldy), (f32, rows, None)
+        if p.op == NM_ROWS_RMSNORM:
+            self._norm_call = self._call("nm_rmsnorm", 0, *x_specs, (io, self._y, p.ldr), (io, self._y[1:], None),
+                                         (io, self._y, p.ldh), *y_specs)
+        else:
+            self._gate_call = self._call("nm_swiglu", 0, *x_specs, *y_specs)
 
 
 def nm_rows_plan_init(rows, cols, op="rmsnorm", dtype="f16", x_dtype=None, y_dtype=None, ldx=None, ldr=None, ldh=None,
@@ -427,6 +447,10 @@ def nm_rows_plan_init(rows, cols, op="rmsnorm", dtype="f16", x_dtype=None, y_dty
 def nm_rmsnorm(plan, dX, d_gamma, dY, y_scale=None, residual=None, h=None, row_scale=None, col_scale=None,
                stream=None):
     """y = (x + residual) * gamma / sqrt(mean((x + residual)^2) + eps) by rows; h receives x + residual."""
+    call = plan._norm_call
+    status = call(dX, row_scale, col_scale, residual, d_gamma, h, dY, y_scale, stream) if call else -1
+    if status >= 0:
+        return _check(status)
     dev, stream = _where(dX, stream)
     ldx, ldr, ldh, ldy = plan._strides
     shape, io, f32 = plan._y, plan.io_dtype, torch.float32
@@ -441,6 +465,10 @@ def nm_rmsnorm(plan, dX, d_gamma, dY, y_scale=None, residual=None, h=None, row_s
 
 def nm_swiglu(plan, dX, dY, y_scale=None, row_scale=None, col_scale=None, stream=None):
     """y = silu(gate) * up by rows, gate and up the halves of x's columns."""
+    call = plan._gate_call
+    status = call(dX, row_scale, col_scale, dY, y_scale, stream) if call else -1
+    if status >= 0:
+        return _check(status)
     dev, stream = _where(dX, stream)
     ldx, _, _, ldy = plan._strides
     shape, f32 = plan._y, torch.float32
@@ -469,6 +497,9 @@ class W4Plan(_LayerPlan):
         self.code_ld, self.meta_ld = code_ld.value, meta_ld.value
         self._x, self._y, self._packed = (p.n, p.k), (p.n, p.m), (size.value,)
         self._strides = (p.ldx, p.ldy)
+        self._product_call = self._call(
+            "nm_w4_matvec", 1, (torch.uint8, self._packed, None), (self.x_dtype, self._x, p.ldx),
+            (torch.float32, self._x[:1], None), (self.y_dtype, self._y, p.ldy))
 
     def empty_packed(self, device="cuda"):
         return torch.empty((self.packed_bytes,), dtype=torch.uint8, device=device)
@@ -504,6 +535,10 @@ def nm_w4_pack(plan, d_codes, d_scales, d_packed, zeros=None, meta=None, stream=
 
 def nm_w4_matvec(plan, d_packed, dX, dY, x_scale=None, stream=None):
     """y (n x m) = x (n x k) times the packed W (m x k) transposed."""
+    call = plan._product_call
+    status = call(d_packed, dX, x_scale, dY, stream) if call else -1
+    if status >= 0:
+        return _check(status)
     dev, stream = _where(dX, stream)
     ldx, ldy = plan._strides
     _check(lib().nm_w4_matvec(

@@ -21,6 +21,7 @@ SOURCES = ["nm_api.hip", "nm_prune.hip", "nm_rows.hip", "nm_vw.hip", "nm_gemm.hi
            "nm_gemm_i8.hip",
            "nm_skinny_f16.hip", "nm_skinny_bf16.hip", "nm_skinny_i8.hip",
            "nm_rowops.hip", "nm_w4.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip", "nm_w4_i8.hip", "nm_w4_i8_bf16.hip"]
+CALL_LIB = os.path.join(HERE, "_nmcall.so")       # operand checks and calls of the layer operators (Python extension)
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 CLANG = os.path.join(ROCM, "llvm", "bin", "clang++")
@@ -145,13 +146,32 @@ def _link(objs, out, soname):
     os.replace(tmp, out)
 
 
+def _build_call():
+    """The Python extension, against the installed torch (host code only)."""
+    import sysconfig
+    import torch
+    tl, tmp = torch_lib_dir(), CALL_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I" + os.path.join(os.path.dirname(tl), "include"), "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "nm_call.cpp"), "-o", tmp, "-L" + tl, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath," + tl]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, CALL_LIB)
+
+
 def build(verbose=True):
-    """Compile every HIP source for gfx950 and link libnmsparse.so and libnmcal.so (always rebuilds)."""
+    """Compile every HIP source for gfx950 and link libnmsparse.so and libnmcal.so, and the Python extension
+    _nmcall.so (always rebuilds)."""
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 2) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 3) as ex:
         m0 = ex.submit(_m0_check)
+        call = ex.submit(_build_call)
         objs = list(ex.map(_compile, SOURCES + ["nm_calib.hip"]))
         m0.result()
+        call.result()
     _link(objs[-1:], CAL_LIB, "libnmcal.so")
     objs = objs[:-1]
     tl = torch_lib_dir()
