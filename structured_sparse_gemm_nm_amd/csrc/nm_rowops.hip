@@ -5,7 +5,7 @@
 // Both are one pass over memory: a row is read once into registers, its
 // statistics (the sum of squares, the largest magnitude) are reduced over the
 // row's threads, and the row is written. Rows too long for that are read twice,
-// the second time from the caches.
+// the second time from the caches. Memory bounds them (figures at row_op_kernel).
 #include <math.h>
 
 #include <new>
@@ -33,57 +33,49 @@ struct RowArgs {
 };
 
 constexpr int ROW_V = 8;          // columns a thread takes at a time
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_MOST = 1024;    // threads a row
 
 // 16 bytes at an address that may be off the 16-byte grid (the up half of a
 // row starts at any column)
 struct __attribute__((packed, aligned(2))) U16x8 { u32x4 v; };
-struct __attribute__((packed, aligned(4))) U32x4 { u32x4 v; };
 
-// ROW_V columns from column c of a row of `cols`, in fp32; columns past the end are 0.
+// ROW_V columns of a row as they lie in memory. The loads of a row are all on
+// their way before the first is used, so they are free of branches: a thread whose
+// columns do not fit loads the row's first ones and takes `part` instead.
+template <int W> struct RowRaw { u32x4 v[W / 4]; };   // W dwords
+
+template <int W>
+__device__ __forceinline__ RowRaw<W> row_raw(const void* at) {
+  RowRaw<W> r;
+#pragma unroll
+  for (int i = 0; i < W / 4; i++) r.v[i] = ((const U16x8*)at)[i].v;
+  return r;
+}
+
 template <int IO>
-__device__ __forceinline__ void load16(float (&o)[ROW_V], const uint16_t* row, int64_t c, int64_t cols) {
-  if (c + ROW_V <= cols) {
-    const u32x4 v = ((const U16x8*)(row + c))->v;
+__device__ __forceinline__ void unpack16(float (&o)[ROW_V], const RowRaw<4>& r) {
 #pragma unroll
-    for (int i = 0; i < ROW_V; i++) o[i] = from_bits16<IO>((uint16_t)(v[i / 2] >> (16 * (i % 2))));
-  } else {
-#pragma unroll
-    for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? from_bits16<IO>(row[c + i]) : 0.0f;
-  }
+  for (int i = 0; i < ROW_V; i++) o[i] = from_bits16<IO>((uint16_t)(r.v[0][i / 2] >> (16 * (i % 2))));
 }
 template <typename T>
-__device__ __forceinline__ void load32(T (&o)[ROW_V], const T* row, int64_t c, int64_t cols) {
-  if (c + ROW_V <= cols) {
+__device__ __forceinline__ void unpack32(T (&o)[ROW_V], const RowRaw<8>& r) {
 #pragma unroll
-    for (int i = 0; i < ROW_V; i += 4) {
-      const u32x4 v = ((const U32x4*)(row + c + i))->v;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const uint32_t bits = v[j];   // by itself: a bit cast of v[j] in place reads v[0]
-        o[i + j] = __builtin_bit_cast(T, bits);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? row[c + i] : (T)0;
+  for (int i = 0; i < ROW_V; i++) {
+    const uint32_t bits = r.v[i / 4][i % 4];   // by itself: a bit cast of the element in place reads the first
+    o[i] = __builtin_bit_cast(T, bits);
   }
 }
 
-// ROW_V values of x at column c of a row: 16-bit, or an accumulator times both scales.
-template <int IO, bool ACC>
-__device__ __forceinline__ void load_x(float (&o)[ROW_V], const RowArgs& A, int64_t row, float rs, int64_t first,
-                                       int64_t c) {
-  if constexpr (ACC) {
-    int32_t a[ROW_V];
-    float cs[ROW_V];
-    load32<int32_t>(a, (const int32_t*)A.x + row * A.ldx + first, c, A.cols);
-    load32<float>(cs, A.col_scale + first, c, A.cols);
+// The same columns where the row ends among them; those past the end are 0.
+template <int IO>
+__device__ __forceinline__ void part16(float (&o)[ROW_V], const uint16_t* row, int64_t c, int64_t cols) {
 #pragma unroll
-    for (int i = 0; i < ROW_V; i++) o[i] = (float)a[i] * rs * cs[i];
-  } else {
-    load16<IO>(o, (const uint16_t*)A.x + row * A.ldx + first, c, A.cols);
-  }
+  for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? from_bits16<IO>(row[c + i]) : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ void part32(T (&o)[ROW_V], const T* row, int64_t c, int64_t cols) {
+#pragma unroll
+  for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? row[c + i] : (T)0;
 }
 
 // silu(g) * u. exp of -|g| neither overflows nor divides by a large number; as
@@ -112,8 +104,8 @@ __device__ __forceinline__ void store16(uint16_t* row, int64_t c, int64_t cols, 
   }
 }
 
-// round(v * r) in 8 bits; r = 127 / (largest magnitude) may be infinite (a row
-// of zeros or of the smallest values): NaN converts to 0, the rest is clamped.
+// round(v * r) in 8 bits, r = 127 / (largest magnitude), infinite for a row of
+// zeros: NaN converts to 0, the rest is clamped.
 __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, const float (&v)[ROW_V], float r) {
   uint32_t o[ROW_V];
 #pragma unroll
@@ -134,86 +126,173 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, co
 // of |v|, which order as the values do and put a NaN above infinity, so that it
 // reaches the scale.
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
-  __shared__ float ps[16];
-  __shared__ uint32_t pt[16];
+  __shared__ float ps[ROW_MOST / 64];
+  __shared__ uint32_t pt[ROW_MOST / 64];
   for (int o = 32; o > 0; o >>= 1) {
     sum += __shfl_xor(sum, o);
     top = max(top, (uint32_t)__shfl_xor((int)top, o));
   }
   const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+  if (n == 1) return;
   if ((threadIdx.x & 63) == 0) { ps[w] = sum; pt[w] = top; }
   __syncthreads();
   sum = 0.0f;
   for (int i = 0; i < n; i++) { sum += ps[i]; top = max(top, pt[i]); }
 }
 
-// One block a row. C > 0: the row sits in C pieces of ROW_V columns a thread;
-// C = 0: any length, read twice.
-template <int OP, int IO, bool ACC, bool Y8, int C>
-__global__ void __launch_bounds__(ROW_THREADS) row_op_kernel(RowArgs A) {
-  const int64_t row = blockIdx.x;
-  const float rs = ACC ? A.row_scale[row] : 1.0f;
+// What a thread loads for ROW_V columns: x (for the activation the gate), the
+// second operand (the residual; the up half), and what the rows have in common
+// (gamma and, for accumulators, the column scales).
+template <int OP, bool ACC> struct RowPiece {
+  RowRaw<ACC ? 8 : 4> x;
+  RowRaw<OP == NM_ROWS_SWIGLU && ACC ? 8 : 4> second;
+  RowRaw<4> gamma;
+  RowRaw<8> cs[OP == NM_ROWS_SWIGLU ? 2 : 1];
+};
 
-  // v before the row's factor; the norm's u goes to h and into the sum
-  auto make = [&](float (&v)[ROW_V], int64_t c, float& sum, bool write_h) {
-    load_x<IO, ACC>(v, A, row, rs, 0, c);
-    if constexpr (OP == NM_ROWS_RMSNORM) {
-      float g[ROW_V];
-      if (A.residual) {
-        float r[ROW_V];
-        load16<IO>(r, A.residual + row * A.ldr, c, A.cols);
+// One block a row. C > 0: the row sits in C pieces of ROW_V columns a thread;
+// C = 0: any length, read twice. A row gets as many threads as it has pieces, up to
+// 1024, and then two or four pieces each: with 256 threads and up to eight pieces, each
+// waiting for its own loads, the norm of 8192x4096 took 47 us, the activation
+// 6.6 for 16x11008 and 94 for 4096x11008 accumulators. Memory bounds it: norm of
+// 8192x4096 in 8 bits 43 us (235 MB, 5.5 TB/s), of 4096x4096 accumulators 32 (168 MB,
+// 5.2 TB/s), activation of 4096x11008 accumulators 84 (406 MB, 4.8 TB/s); few rows
+// by latency: 16x11008 5.0 us, one row of 4096 4.5.
+template <int OP, int IO, bool ACC, bool Y8, int C>
+__global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
+  constexpr bool NORM = OP == NM_ROWS_RMSNORM;
+  typedef RowPiece<OP, ACC> piece_t;
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= A.rows) return;
+  const float rs = ACC ? A.row_scale[row] : 1.0f;
+  const uint8_t* const x = A.x + row * A.ldx * (ACC ? 4 : 2);
+  const uint16_t* const res = A.residual ? A.residual + row * A.ldr : nullptr;
+  constexpr int XS = ACC ? 4 : 2;
+
+  auto load_scales = [&](piece_t& P, int64_t at) {
+    if constexpr (ACC) {
+      P.cs[0] = row_raw<8>(A.col_scale + at);
+      if constexpr (!NORM) P.cs[1] = row_raw<8>(A.col_scale + A.cols + at);
+    }
+  };
+  // Column scales lie in the caches. With two pieces a thread they come last, or their
+  // registers would leave a CU one block (4096x11008 accumulators: 96 us, so 84).
+  constexpr bool LATE = ACC && C > 1;
+  auto load = [&](piece_t& P, int64_t c) {
+    const int64_t at = c + ROW_V <= A.cols ? c : 0;
+    P.x = row_raw<ACC ? 8 : 4>(x + at * XS);
+    if constexpr (NORM) {
+      if (res) P.second = row_raw<4>(res + at);
+      P.gamma = row_raw<4>(A.gamma + at);
+    } else {
+      P.second = row_raw<ACC ? 8 : 4>(x + (A.cols + at) * XS);
+    }
+    if constexpr (!LATE) load_scales(P, at);
+  };
+  auto value = [&](float (&o)[ROW_V], const RowRaw<ACC ? 8 : 4>& raw, const RowRaw<8>& scales) {
+    if constexpr (ACC) {
+      int32_t a[ROW_V];
+      float cs[ROW_V];
+      unpack32(a, raw);
+      unpack32(cs, scales);
 #pragma unroll
-        for (int i = 0; i < ROW_V; i++) v[i] += r[i];
+      for (int i = 0; i < ROW_V; i++) o[i] = (float)a[i] * rs * cs[i];
+    } else {
+      unpack16<IO>(o, raw);
+    }
+  };
+  auto value_part = [&](float (&o)[ROW_V], int64_t first, int64_t c) {
+    if constexpr (ACC) {
+      int32_t a[ROW_V];
+      float cs[ROW_V];
+      part32(a, (const int32_t*)x + first, c, A.cols);
+      part32(cs, A.col_scale + first, c, A.cols);
+#pragma unroll
+      for (int i = 0; i < ROW_V; i++) o[i] = (float)a[i] * rs * cs[i];
+    } else {
+      part16<IO>(o, (const uint16_t*)x + first, c, A.cols);
+    }
+  };
+
+  // v before the row's factor, of columns that exist; the norm's u goes to h and into the sum
+  auto make = [&](float (&v)[ROW_V], piece_t& P, int64_t c, float& sum, uint32_t& top, bool write_h) {
+    float s[ROW_V], g[ROW_V];
+    if (c + ROW_V <= A.cols) {
+      if constexpr (LATE) load_scales(P, c);
+      value(v, P.x, P.cs[0]);
+      if constexpr (NORM) {
+        if (res) unpack16<IO>(s, P.second);
+        unpack16<IO>(g, P.gamma);
+      } else {
+        value(s, P.second, P.cs[1]);
+      }
+    } else {
+      value_part(v, 0, c);
+      if constexpr (NORM) {
+        if (res) part16<IO>(s, res, c, A.cols);
+        part16<IO>(g, A.gamma, c, A.cols);
+      } else {
+        value_part(s, A.cols, c);
+      }
+    }
+    if constexpr (NORM) {
+      if (res) {
+#pragma unroll
+        for (int i = 0; i < ROW_V; i++) v[i] += s[i];
       }
       if (write_h && A.h) store16<IO>(A.h + row * A.ldh, c, A.cols, v);
-      load16<IO>(g, A.gamma, c, A.cols);
 #pragma unroll
       for (int i = 0; i < ROW_V; i++) {
         sum = __builtin_fmaf(v[i], v[i], sum);
         v[i] *= g[i];
       }
     } else {
-      float u[ROW_V];
-      load_x<IO, ACC>(u, A, row, rs, A.cols, c);
 #pragma unroll
-      for (int i = 0; i < ROW_V; i++) v[i] = gated(v[i], u[i]);
+      for (int i = 0; i < ROW_V; i++) v[i] = gated(v[i], s[i]);
     }
-  };
-  auto largest = [&](const float (&v)[ROW_V], uint32_t& top) {
     if constexpr (Y8) {
 #pragma unroll
       for (int i = 0; i < ROW_V; i++) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
     }
   };
 
+  const int64_t first = (int64_t)threadIdx.x * ROW_V, stride = (int64_t)blockDim.x * ROW_V;
   float sum = 0.0f;
   uint32_t top = 0;
   float v[C > 0 ? C : 1][ROW_V];
   if constexpr (C > 0) {
+    piece_t P[C];
+    if (A.cols >= ROW_V) {
 #pragma unroll
-    for (int p = 0; p < C; p++) {
-      const int64_t c = (int64_t)(p * ROW_THREADS + threadIdx.x) * ROW_V;
-      if (c < A.cols) {
-        make(v[p], c, sum, true);
-        largest(v[p], top);
-      }
+      for (int p = 0; p < C; p++) load(P[p], first + p * stride);
     }
+#pragma unroll
+    for (int p = 0; p < C; p++)
+      if (first + p * stride < A.cols) make(v[p], P[p], first + p * stride, sum, top, true);
   } else {
-    for (int64_t c = (int64_t)threadIdx.x * ROW_V; c < A.cols; c += ROW_THREADS * ROW_V) {
-      make(v[0], c, sum, false);
-      largest(v[0], top);
+    for (int64_t c = first; c < A.cols; c += stride) {
+      piece_t P;
+      load(P, c);
+      make(v[0], P, c, sum, top, false);
     }
   }
   float f = 1.0f, r = 0.0f;
-  if constexpr (OP == NM_ROWS_RMSNORM || Y8) row_reduce(sum, top);
-  if constexpr (OP == NM_ROWS_RMSNORM) f = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, A.rcols, A.eps));
+  bool small = false;
+  if constexpr (NORM || Y8) row_reduce(sum, top);
+  if constexpr (NORM) f = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, A.rcols, A.eps));
   if constexpr (Y8) {
-    const float a = __builtin_bit_cast(float, top);
-    r = 127.0f / a;
+    float a = __builtin_bit_cast(float, top);
     if (threadIdx.x == 0) A.y_scale[row] = a * f / 127.0f;
+    small = a < 0x1p-64f;              // 127 / a may be past fp32: both by 2^64
+    if (small) a *= 0x1p64f;
+    r = 127.0f / a;
   }
   auto write = [&](float (&w)[ROW_V], int64_t c) {
     if constexpr (Y8) {
+      if (small) {
+#pragma unroll
+        for (int i = 0; i < ROW_V; i++) w[i] *= 0x1p64f;
+      }
       store8(A.y + row * A.ldy, c, A.cols, w, r);
     } else {
 #pragma unroll
@@ -223,33 +302,39 @@ __global__ void __launch_bounds__(ROW_THREADS) row_op_kernel(RowArgs A) {
   };
   if constexpr (C > 0) {
 #pragma unroll
-    for (int p = 0; p < C; p++) {
-      const int64_t c = (int64_t)(p * ROW_THREADS + threadIdx.x) * ROW_V;
-      if (c < A.cols) write(v[p], c);
-    }
+    for (int p = 0; p < C; p++)
+      if (first + p * stride < A.cols) write(v[p], first + p * stride);
   } else {
-    for (int64_t c = (int64_t)threadIdx.x * ROW_V; c < A.cols; c += ROW_THREADS * ROW_V) {
+    for (int64_t c = first; c < A.cols; c += stride) {
       float unused = 0.0f;
-      make(v[0], c, unused, true);
+      uint32_t none = 0;
+      piece_t P;
+      load(P, c);
+      make(v[0], P, c, unused, none, true);
       write(v[0], c);
     }
   }
 }
 
 template <int OP, int IO, bool ACC, bool Y8, int C>
-hipError_t row_go(const RowArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C>), dim3((unsigned)a.rows), dim3(ROW_THREADS), 0, s, a);
+hipError_t row_go(const RowArgs& a, int threads, hipStream_t s) {
+  // a grid dimension holds under 2^32 threads
+  const int64_t across = a.rows < ((int64_t)1 << 20) ? a.rows : (int64_t)1 << 20;
+  hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C>), dim3((unsigned)across, (unsigned)((a.rows + across - 1) / across)),
+                     dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 
 template <int OP, int IO, bool ACC, bool Y8>
 hipError_t row_len(const RowArgs& a, hipStream_t s) {
-  const int64_t per = ROW_THREADS * ROW_V;
-  if (a.cols <= per) return row_go<OP, IO, ACC, Y8, 1>(a, s);
-  if (a.cols <= 2 * per) return row_go<OP, IO, ACC, Y8, 2>(a, s);
-  if (a.cols <= 4 * per) return row_go<OP, IO, ACC, Y8, 4>(a, s);
-  if (a.cols <= 8 * per) return row_go<OP, IO, ACC, Y8, 8>(a, s);
-  return row_go<OP, IO, ACC, Y8, 0>(a, s);
+  const int64_t pieces = (a.cols + ROW_V - 1) / ROW_V;
+  auto threads = [&](int c) { return (int)((pieces + 64 * c - 1) / (64 * c)) * 64; };
+  if (pieces <= ROW_MOST) return row_go<OP, IO, ACC, Y8, 1>(a, threads(1), s);
+  if (pieces <= 2 * ROW_MOST) return row_go<OP, IO, ACC, Y8, 2>(a, threads(2), s);
+  if constexpr (!ACC) {
+    if (pieces <= 4 * ROW_MOST) return row_go<OP, IO, ACC, Y8, 4>(a, threads(4), s);
+  }
+  return row_go<OP, IO, ACC, Y8, 0>(a, ROW_MOST, s);
 }
 
 template <int OP, int IO>
@@ -335,7 +420,6 @@ nm_status_t nm_rows_plan_init(nm_rows_plan_t* plan, const nm_rows_problem_t* p) 
   if (norm && !(isfinite(p->eps) && p->eps >= 0.0f))
     return row_fail(NM_ERR_INVALID_ARG, "eps must be finite and >= 0");
   if (p->rows < 0 || p->cols < 0) return row_fail(NM_ERR_SHAPE, "rows and cols must be >= 0");
-  // the grid: one block of 256 threads a row, under 2^32 threads
   if (p->rows >= ((int64_t)1 << 24) || p->cols > ((int64_t)1 << 30))
     return row_fail(NM_ERR_SHAPE, "rows must be < 2^24 and cols <= 2^30");
   const int64_t limit = (int64_t)1 << 46, width = norm ? p->cols : 2 * p->cols;
