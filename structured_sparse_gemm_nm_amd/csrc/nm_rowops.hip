@@ -122,22 +122,50 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, co
   }
 }
 
+// v of another lane of the 16 that lane l shares a row of the wave with
+template <int CTRL> __device__ __forceinline__ uint32_t row_dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+// Sum and largest over 16 lanes, in each of them: neighbours, pairs, then the
+// halves of 8 and of 16 mirrored.
+__device__ __forceinline__ void reduce16(float& sum, uint32_t& top) {
+  auto step = [&](uint32_t s, uint32_t t) {
+    sum += __builtin_bit_cast(float, s);
+    top = max(top, t);
+  };
+  const auto bits = [&] { return __builtin_bit_cast(uint32_t, sum); };
+  step(row_dpp<0xB1>(bits()), row_dpp<0xB1>(top));
+  step(row_dpp<0x4E>(bits()), row_dpp<0x4E>(top));
+  step(row_dpp<0x141>(bits()), row_dpp<0x141>(top));
+  step(row_dpp<0x140>(bits()), row_dpp<0x140>(top));
+}
+
 // Sum and largest magnitude over the block. Magnitudes are compared as the bits
 // of |v|, which order as the values do and put a NaN above infinity, so that it
-// reaches the scale.
+// reaches the scale. Within 16 lanes without LDS, and one read of it for the waves'
+// shares: for a single row the time is the sum of such latencies.
 __device__ __forceinline__ void row_reduce(float& sum, uint32_t& top) {
-  __shared__ float ps[ROW_MOST / 64];
-  __shared__ uint32_t pt[ROW_MOST / 64];
-  for (int o = 32; o > 0; o >>= 1) {
-    sum += __shfl_xor(sum, o);
-    top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  __shared__ u32x2 part[ROW_MOST / 64];
+  reduce16(sum, top);
+  const int bits = (int)__builtin_bit_cast(uint32_t, sum);
+  float s[4];
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    s[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, 16 * i));
+    t = max(t, (uint32_t)__builtin_amdgcn_readlane((int)top, 16 * i));
   }
-  const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+  sum = (s[0] + s[1]) + (s[2] + s[3]);
+  top = t;
+  const int n = blockDim.x >> 6, l16 = threadIdx.x & 15;
   if (n == 1) return;
-  if ((threadIdx.x & 63) == 0) { ps[w] = sum; pt[w] = top; }
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = u32x2{__builtin_bit_cast(uint32_t, sum), top};
   __syncthreads();
-  sum = 0.0f;
-  for (int i = 0; i < n; i++) { sum += ps[i]; top = max(top, pt[i]); }
+  const u32x2 w = l16 < n ? part[l16] : u32x2{0, 0};
+  const uint32_t ws = w[0];
+  sum = __builtin_bit_cast(float, ws);
+  top = w[1];
+  reduce16(sum, top);
 }
 
 // What a thread loads for ROW_V columns: x (for the activation the gate), the
@@ -157,7 +185,7 @@ template <int OP, bool ACC> struct RowPiece {
 // 6.6 for 16x11008 and 94 for 4096x11008 accumulators. Memory bounds it: norm of
 // 8192x4096 in 8 bits 43 us (235 MB, 5.5 TB/s), of 4096x4096 accumulators 32 (168 MB,
 // 5.2 TB/s), activation of 4096x11008 accumulators 84 (406 MB, 4.8 TB/s); few rows
-// by latency: 16x11008 5.0 us, one row of 4096 4.5.
+// by latency: 16x11008 4.4 us, one row of 4096 2.6.
 template <int OP, int IO, bool ACC, bool Y8, int C>
 __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   constexpr bool NORM = OP == NM_ROWS_RMSNORM;
