@@ -40,8 +40,8 @@ constexpr int ROW_MOST = 1024;    // threads a row
 struct __attribute__((packed, aligned(2))) U16x8 { u32x4 v; };
 
 // ROW_V columns of a row as they lie in memory. The loads of a row are all on
-// their way before the first is used, so they are free of branches: a thread whose
-// columns do not fit loads the row's first ones and takes `part` instead.
+// their way before the first is used, so they are free of branches: a thread past
+// the last whole piece loads the row's last ROW_V columns and shifts its own down.
 template <int W> struct RowRaw { u32x4 v[W / 4]; };   // W dwords
 
 template <int W>
@@ -66,7 +66,21 @@ __device__ __forceinline__ void unpack32(T (&o)[ROW_V], const RowRaw<8>& r) {
   }
 }
 
-// The same columns where the row ends among them; those past the end are 0.
+// The columns from k on, zeros behind them: 16-bit and 32-bit columns.
+__device__ __forceinline__ void row_shift(RowRaw<4>& r, int k) {
+  u32x4& v = r.v[0];
+  if (k & 4) v = u32x4{v[2], v[3], 0, 0};
+  if (k & 2) v = u32x4{v[1], v[2], v[3], 0};
+  if (k & 1) v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+}
+__device__ __forceinline__ void row_shift(RowRaw<8>& r, int k) {
+  u32x4 &a = r.v[0], &b = r.v[1];
+  if (k & 4) { a = b; b = u32x4{0, 0, 0, 0}; }
+  if (k & 2) { a = u32x4{a[2], a[3], b[0], b[1]}; b = u32x4{b[2], b[3], 0, 0}; }
+  if (k & 1) { a = u32x4{a[1], a[2], a[3], b[0]}; b = u32x4{b[1], b[2], b[3], 0}; }
+}
+
+// The same columns of a row of fewer than ROW_V; those past the end are 0.
 template <int IO>
 __device__ __forceinline__ void part16(float (&o)[ROW_V], const uint16_t* row, int64_t c, int64_t cols) {
 #pragma unroll
@@ -87,12 +101,12 @@ __device__ __forceinline__ float gated(float g, float u) {
   return g * (g < 0.0f ? e * r : r) * u;
 }
 
-template <int IO>
+template <int IO, bool TAIL>
 __device__ __forceinline__ void store16(uint16_t* row, int64_t c, int64_t cols, const float (&v)[ROW_V]) {
   uint16_t o[ROW_V];
 #pragma unroll
   for (int i = 0; i < ROW_V; i++) o[i] = to_bits16<IO>(v[i]);
-  if (c + ROW_V <= cols) {
+  if (!TAIL || c + ROW_V <= cols) {
     u32x4 w;
 #pragma unroll
     for (int i = 0; i < 4; i++) w[i] = (uint32_t)o[2 * i] | (uint32_t)o[2 * i + 1] << 16;
@@ -106,6 +120,7 @@ __device__ __forceinline__ void store16(uint16_t* row, int64_t c, int64_t cols, 
 
 // round(v * r) in 8 bits, r = 127 / (largest magnitude), infinite for a row of
 // zeros: NaN converts to 0, the rest is clamped.
+template <bool TAIL>
 __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, const float (&v)[ROW_V], float r) {
   uint32_t o[ROW_V];
 #pragma unroll
@@ -113,7 +128,7 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, co
     const float t = __builtin_rintf(v[i] * r);
     o[i] = t != t ? 0u : (uint32_t)(int)__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) & 0xFFu;
   }
-  if (c + ROW_V <= cols) {
+  if (!TAIL || c + ROW_V <= cols) {
     *(u32x2*)(row + c) = u32x2{o[0] | o[1] << 8 | o[2] << 16 | o[3] << 24, o[4] | o[5] << 8 | o[6] << 16 | o[7] << 24};
   } else {
 #pragma unroll
@@ -179,14 +194,17 @@ template <int OP, bool ACC> struct RowPiece {
 };
 
 // One block a row. C > 0: the row sits in C pieces of ROW_V columns a thread;
-// C = 0: any length, read twice. A row gets as many threads as it has pieces, up to
-// 1024, and then two or four pieces each: with 256 threads and up to eight pieces, each
-// waiting for its own loads, the norm of 8192x4096 took 47 us, the activation
-// 6.6 for 16x11008 and 94 for 4096x11008 accumulators. Memory bounds it: norm of
-// 8192x4096 in 8 bits 43 us (235 MB, 5.5 TB/s), of 4096x4096 accumulators 32 (168 MB,
-// 5.2 TB/s), activation of 4096x11008 accumulators 84 (406 MB, 4.8 TB/s); few rows
-// by latency: 16x11008 4.4 us, one row of 4096 2.6.
-template <int OP, int IO, bool ACC, bool Y8, int C>
+// C = 0: any length, read twice. TAIL: the columns are no whole pieces (one row of
+// 4095, 16 bits: 3.8 us, and 4.5 with the last columns loaded one by one; with the
+// shifts in every kernel the norm of 4096x16384 takes 96 us, without 83). A row
+// gets as many threads as it has pieces, up to 1024, and then two or four pieces each:
+// with 256 threads and up to eight pieces, each waiting for its own loads, the norm
+// of 8192x4096 took 47 us, the activation 6.6 for 16x11008 and 94 for 4096x11008
+// accumulators. Memory bounds it: norm of 8192x4096 in 8 bits 41 us (235 MB, 5.7 TB/s),
+// of 4096x4096 accumulators 31 (168 MB, 5.4 TB/s), activation of 4096x11008
+// accumulators 82 (406 MB, 5.0 TB/s); few rows by latency: 16x11008 4.4 us, one row
+// of 4096 2.6.
+template <int OP, int IO, bool ACC, bool Y8, int C, bool TAIL>
 __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   constexpr bool NORM = OP == NM_ROWS_RMSNORM;
   typedef RowPiece<OP, ACC> piece_t;
@@ -207,7 +225,7 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   // registers would leave a CU one block (4096x11008 accumulators: 96 us, so 84).
   constexpr bool LATE = ACC && C > 1;
   auto load = [&](piece_t& P, int64_t c) {
-    const int64_t at = c + ROW_V <= A.cols ? c : 0;
+    const int64_t at = TAIL ? min(c, A.cols - ROW_V) : c < A.cols ? c : 0;
     P.x = row_raw<ACC ? 8 : 4>(x + at * XS);
     if constexpr (NORM) {
       if (res) P.second = row_raw<4>(res + at);
@@ -245,8 +263,18 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   // v before the row's factor, of columns that exist; the norm's u goes to h and into the sum
   auto make = [&](float (&v)[ROW_V], piece_t& P, int64_t c, float& sum, uint32_t& top, bool write_h) {
     float s[ROW_V], g[ROW_V];
-    if (c + ROW_V <= A.cols) {
-      if constexpr (LATE) load_scales(P, c);
+    if (!TAIL || A.cols >= ROW_V) {
+      if constexpr (LATE) load_scales(P, TAIL ? min(c, A.cols - ROW_V) : c);
+      if (TAIL && c + ROW_V > A.cols) {
+        const int k = (int)(c + ROW_V - A.cols);
+        row_shift(P.x, k);
+        if (!NORM || res) row_shift(P.second, k);
+        if constexpr (NORM) row_shift(P.gamma, k);
+        if constexpr (ACC) {
+          row_shift(P.cs[0], k);
+          if constexpr (!NORM) row_shift(P.cs[1], k);
+        }
+      }
       value(v, P.x, P.cs[0]);
       if constexpr (NORM) {
         if (res) unpack16<IO>(s, P.second);
@@ -268,7 +296,7 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
 #pragma unroll
         for (int i = 0; i < ROW_V; i++) v[i] += s[i];
       }
-      if (write_h && A.h) store16<IO>(A.h + row * A.ldh, c, A.cols, v);
+      if (write_h && A.h) store16<IO, TAIL>(A.h + row * A.ldh, c, A.cols, v);
 #pragma unroll
       for (int i = 0; i < ROW_V; i++) {
         sum = __builtin_fmaf(v[i], v[i], sum);
@@ -290,9 +318,10 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   float v[C > 0 ? C : 1][ROW_V];
   if constexpr (C > 0) {
     piece_t P[C];
-    if (A.cols >= ROW_V) {
+    if (!TAIL || A.cols >= ROW_V) {
 #pragma unroll
       for (int p = 0; p < C; p++) load(P[p], first + p * stride);
+      asm volatile("" ::: "memory");   // and here, not where they are used
     }
 #pragma unroll
     for (int p = 0; p < C; p++)
@@ -321,11 +350,11 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
 #pragma unroll
         for (int i = 0; i < ROW_V; i++) w[i] *= 0x1p64f;
       }
-      store8(A.y + row * A.ldy, c, A.cols, w, r);
+      store8<TAIL>(A.y + row * A.ldy, c, A.cols, w, r);
     } else {
 #pragma unroll
       for (int i = 0; i < ROW_V; i++) w[i] *= f;
-      store16<IO>((uint16_t*)A.y + row * A.ldy, c, A.cols, w);
+      store16<IO, TAIL>((uint16_t*)A.y + row * A.ldy, c, A.cols, w);
     }
   };
   if constexpr (C > 0) {
@@ -348,8 +377,9 @@ template <int OP, int IO, bool ACC, bool Y8, int C>
 hipError_t row_go(const RowArgs& a, int threads, hipStream_t s) {
   // a grid dimension holds under 2^32 threads
   const int64_t across = a.rows < ((int64_t)1 << 20) ? a.rows : (int64_t)1 << 20;
-  hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C>), dim3((unsigned)across, (unsigned)((a.rows + across - 1) / across)),
-                     dim3(threads), 0, s, a);
+  const dim3 grid((unsigned)across, (unsigned)((a.rows + across - 1) / across));
+  if (a.cols % ROW_V) hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C, true>), grid, dim3(threads), 0, s, a);
+  else hipLaunchKernelGGL((row_op_kernel<OP, IO, ACC, Y8, C, false>), grid, dim3(threads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -94,15 +94,15 @@ def test_blocks_chain_on_accumulators():
     a, _, _ = block(128, 256, torch.bfloat16, 3)
     b, _, _ = block(128, 256, torch.bfloat16, 4)
     x, r = inputs(64, 128, torch.bfloat16)
-    y, h = a(x, r)
+    y, h = a(x, r, few=False)
     assert isinstance(y, Rows) and y.values.dtype == torch.int32
-    z, h2 = b(y, h)
+    z, h2 = b(y, h, few=False)
     y16 = y.dense().to(torch.bfloat16)
     u = y.dense().double() + h.double()
     assert ((h2.double() - u).abs() <= HALF[torch.bfloat16] * u.abs() + 2.0 ** -22 * (u.abs() + h.double().abs())).all()
     want, _, _ = exact(b, y.dense(), h, torch.bfloat16, False)
     assert ((z.dense().double().cpu() - want).norm() / want.norm()) < 0.04
-    z16, _ = b(y16, h)
+    z16, _ = b(y16, h, few=False)
     assert ((z16.dense() - z.dense()).norm() / z.dense().norm()) < 0.04
 
 
@@ -118,7 +118,7 @@ def test_weights_are_the_largest_two_of_four_in_sixteen_steps():
         assert ((d - o).abs()[kept] <= (0.5 * w.scale[:, None] + 2.0 ** -10 * o.abs()).expand_as(o)[kept]).all()
 
 
-@pytest.mark.parametrize("n", [3, 64])
+@pytest.mark.parametrize("n", [3, 64, 128])
 def test_captured_calls_repeat(n):
     ff, _, _ = block(128, 256, torch.float16)
     x, r = inputs(n, 128, torch.float16)
