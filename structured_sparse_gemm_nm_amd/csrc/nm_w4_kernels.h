@@ -173,22 +173,29 @@ __device__ __forceinline__ void w4_store(const W4Args& A, floatx4 v, int col, in
 }
 
 // What one tile of k of R row tiles needs from memory; x with it for up to 16 tokens.
-template <int XT, bool SPARSE, int F, int NT, int R> struct W4Tile {
+template <int XT, bool SPARSE, int F, int NT, int R, bool XL> struct W4Tile {
   u32x4 c[R];
   u32x2 mt[R];
   u32x2 sc[R][F];
   uint32_t z[R][F];
-  typename W4Type<XT>::template b<SPARSE> x[NT == 1 ? (XT == DT_I8 ? 2 : 4) : 1];
+  std::conditional_t<XL, u32x4[(XT == DT_I8 ? 2 : 4) * (SPARSE ? 2 : 1)],
+                     typename W4Type<XT>::template b<SPARSE>[NT == 1 ? (XT == DT_I8 ? 2 : 4) : 1]> x;
 };
+
+// Bytes of LDS in which a wave turns a tile of x, 16 tokens 16 bytes apart in their banks.
+constexpr int w4_turn(int tile_bytes) { return 16 * (tile_bytes + 16); }
 
 // What bounds it: the loads of x. They come from the L1 cache, 1 KB (2:4: 2 KB) a
 // matrix instruction against 256 to 512 bytes of codes, so each piece of x serves R row
-// tiles; and R is chosen so that the blocks are whole rounds of the 256 CUs.
+// tiles; and R is chosen so that the blocks are whole rounds of the 256 CUs. The matrix
+// instruction's order has neighbouring lanes load from different tokens, a cache line
+// each; with XL they load a token's row along, and the wave turns the tile in LDS.
 // 16384x4096, one f16 token, 8.5 us with R = 4 (34 MB, 4.1 TB/s; 11.1 with R = 1),
 // 16 tokens 9.3 (18.7); 32768x32768, four 8-bit tokens, 87 us (559 MB, 6.4 TB/s;
 // 115 with R = 1). Codes are loaded past the caches' reuse (nontemporal): x stays there.
-template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R>
+template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R, bool XL>
 __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
+  static_assert(!XL || NT == 1, "x is turned for up to 16 tokens");
   constexpr int ESZ = XT == DT_I8 ? 1 : 2;
   constexpr int S = XT == DT_I8 ? 2 : 4;         // matrix instructions along a tile
   constexpr int SF = S / F;                      // of them, between two scales
@@ -197,7 +204,9 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   constexpr int E = 16 / ESZ;                    // elements of x in 16 bytes
   typedef typename W4Type<XT>::acc acc_t;
   typedef typename W4Type<XT>::template b<SPARSE> b_t;
-  typedef W4Tile<XT, SPARSE, F, NT, R> tile_t;
+  constexpr int TB = TK * ESZ;                   // bytes of a token's row in a tile
+  constexpr int LPR = TB / 16;                   // lanes that load them
+  typedef W4Tile<XT, SPARSE, F, NT, R, XL> tile_t;
   extern __shared__ floatx4 red[];
 
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
@@ -211,12 +220,12 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   const uint8_t* xp[NT];
 #pragma unroll
   for (int j = 0; j < NT; j++)
-    xp[j] = A.x + (int64_t)min(col0 + 16 * j + l16, A.n - 1) * A.ldx * ESZ + q * 16;
+    xp[j] = A.x + (int64_t)min(col0 + 16 * j + l16, A.n - 1) * A.ldx * ESZ;
 
-  // 16 bytes of a token's row at k0 (of the lane's first element); past k the values are zero
-  auto piece = [&](const uint8_t* row, int k0, bool whole) -> u32x4 {
-    const uint8_t* p = row + (size_t)k0 * ESZ;
-    const int left = A.k - k0 - E * q;
+  // the at-th 16 bytes of a token's row from k0 on; past k the values are zero
+  auto piece = [&](const uint8_t* row, int k0, int at, bool whole) -> u32x4 {
+    const uint8_t* p = row + (size_t)k0 * ESZ + at * 16;
+    const int left = A.k - k0 - E * at;
     if (whole || left >= E) return *(const u32x4*)p;
     u32x4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -231,9 +240,9 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   // what one matrix instruction takes of it: one piece, or two half an instruction's k apart
   auto pieces = [&](const uint8_t* row, int k0, bool whole) -> b_t {
     if constexpr (SPARSE)
-      return __builtin_bit_cast(b_t, __builtin_shufflevector(piece(row, k0, whole), piece(row, k0 + KS / 2, whole), 0, 1, 2, 3,
-                                                             4, 5, 6, 7));
-    else return __builtin_bit_cast(b_t, piece(row, k0, whole));
+      return __builtin_bit_cast(b_t, __builtin_shufflevector(piece(row, k0, q, whole), piece(row, k0 + KS / 2, q, whole), 0, 1, 2,
+                                                             3, 4, 5, 6, 7));
+    else return __builtin_bit_cast(b_t, piece(row, k0, q, whole));
   };
 
   auto load = [&](tile_t& T, int t, bool whole) {
@@ -263,7 +272,11 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
         } else T.z[r][f] = 8;
       }
     }
-    if constexpr (NT == 1) {
+    if constexpr (XL) {
+#pragma unroll
+      for (int i = 0; i < 16 * TB / 1024; i++)
+        T.x[i] = piece(A.x + (int64_t)min(i * (64 / LPR) + lane / LPR, A.n - 1) * A.ldx * ESZ, t * TK, lane % LPR, whole);
+    } else if constexpr (NT == 1) {
 #pragma unroll
       for (int i = 0; i < S; i++) T.x[i] = pieces(xp[0], t * TK + i * KS, whole);
     }
@@ -276,7 +289,13 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
 #pragma unroll
     for (int j = 0; j < NT; j++) y[r][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  uint8_t* const turn = (uint8_t*)(red + waves * NT * R * 64) + wave * w4_turn(TB);
   auto compute = [&](const tile_t& T, int t, bool whole) {
+    if constexpr (XL) {
+#pragma unroll
+      for (int i = 0; i < 16 * TB / 1024; i++)
+        *(u32x4*)(turn + (i * (64 / LPR) + lane / LPR) * (TB + 16) + lane % LPR * 16) = T.x[i];
+    }
 #pragma unroll
     for (int f = 0; f < F; f++) {
       if (!whole && t * TK + f * SF * KS >= A.k) break;
@@ -294,7 +313,13 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
         b_t b[NT];
 #pragma unroll
         for (int j = 0; j < NT; j++) {
-          if constexpr (NT == 1) b[j] = T.x[s];
+          if constexpr (XL) {
+            const uint8_t* p = turn + l16 * (TB + 16) + s * KS * ESZ + q * 16;
+            if constexpr (SPARSE)
+              b[j] = __builtin_bit_cast(b_t, __builtin_shufflevector(*(const u32x4*)p, *(const u32x4*)(p + KS / 2 * ESZ), 0, 1,
+                                                                     2, 3, 4, 5, 6, 7));
+            else b[j] = __builtin_bit_cast(b_t, *(const u32x4*)p);
+          } else if constexpr (NT == 1) b[j] = T.x[s];
           else b[j] = pieces(xp[j], t * TK + s * KS, whole);
         }
 #pragma unroll
@@ -553,11 +578,12 @@ __global__ void __launch_bounds__(64 * W4_WALK_WAVES) w4_walk_kernel(W4Args A, W
   } while (base < A.row_tiles);
 }
 
-template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R>
+template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R, bool XL>
 hipError_t w4_go(const W4Args& a, int waves, hipStream_t s) {
-  hipLaunchKernelGGL((w4_kernel<XT, YB, SPARSE, ZEROS, F, NT, R>),
+  constexpr int TB = (SPARSE ? 256 : 128) * (XT == DT_I8 ? 1 : 2);
+  hipLaunchKernelGGL((w4_kernel<XT, YB, SPARSE, ZEROS, F, NT, R, XL>),
                      dim3((unsigned)((a.row_tiles + R - 1) / R), (unsigned)((a.n + 16 * NT - 1) / (16 * NT))),
-                     dim3(64 * waves), (size_t)waves * NT * R * 1024, s, a);
+                     dim3(64 * waves), (size_t)waves * (NT * R * 1024 + (XL ? w4_turn(TB) : 0)), s, a);
   return hipGetLastError();
 }
 
@@ -584,12 +610,18 @@ inline int w4_waves(const W4Args& a, int nt, int r) {
   return w;
 }
 
+// More than four tokens have x turned, where fewer than four row tiles share its loads
+// (2:4 4096x11008, sixteen 8-bit tokens: 7.2 us, 8.8 without; four tokens 6.9 and 6.9;
+// 16384x4096, sixteen f16 tokens: 9.0 and 8.9).
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R>
 hipError_t w4_try(const W4Args& a, int r, hipStream_t s) {
   if constexpr (R > 1) {
     if (r < R) return w4_try<XT, YB, SPARSE, ZEROS, F, NT, R - 1>(a, r, s);
   }
-  return w4_go<XT, YB, SPARSE, ZEROS, F, NT, R>(a, w4_waves(a, NT, R), s);
+  if constexpr (NT == 1 && R <= 3) {
+    if (a.n > 4) return w4_go<XT, YB, SPARSE, ZEROS, F, NT, R, true>(a, w4_waves(a, NT, R), s);
+  }
+  return w4_go<XT, YB, SPARSE, ZEROS, F, NT, R, false>(a, w4_waves(a, NT, R), s);
 }
 
 // The walk: where w4_kernel would hold 32 registers of x a tile, twice, and a CU gets
