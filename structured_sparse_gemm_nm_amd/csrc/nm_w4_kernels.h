@@ -399,7 +399,7 @@ constexpr int W4_WALK_BLOCKS = 512;                // two a CU
 // takes 8 >> ks_log2 row tiles at a time, and 1 << ks_log2 waves share the k of each.
 // What bounds it: the instructions that unpack the codes, together with the start
 // (x has to be in LDS before the first product). 22016x4096 2:4, bf16, one token:
-// 9.3 us, 35 MB at 3.8 TB/s (w4_kernel 11.2; with loads alone, 7.0).
+// 8.9 us, 35 MB at 3.9 TB/s (w4_kernel 11.2; with loads alone, 7.0).
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F>
 __global__ void __launch_bounds__(64 * W4_WALK_WAVES) w4_walk_kernel(W4Args A, W4Walk P) {
   constexpr int ESZ = XT == DT_I8 ? 1 : 2;
@@ -625,13 +625,13 @@ hipError_t w4_try(const W4Args& a, int r, hipStream_t s) {
 }
 
 // The walk: where w4_kernel would hold 32 registers of x a tile, twice, and a CU gets
-// more than four row tiles (22016x4096 2:4: 9.3 against 11.2 us; 12288x4096: 7.7
+// more than four row tiles (22016x4096 2:4: 8.9 against 11.2 us; 12288x4096: 7.7
 // against 7.0), as long as two blocks' x fit a CU's LDS.
 template <int XT, bool YB, bool ZEROS, int F>
 bool w4_walk(const W4Args& a, hipStream_t s, hipError_t& err) {
   const int x_ld = (a.tiles * 512 + 255) / 256 * 256 + 16;   // 16 bytes on: the tokens of a read lie in different banks
   const size_t lds = (size_t)W4_WALK_WAVES * (1024 + W4_SCALE_LDS) + (size_t)a.n * x_ld;
-  if (a.n > 16 || a.row_tiles <= 1024 || lds > 80 * 1024) return false;
+  if (a.n > 16 || a.row_tiles <= 1024 || a.tiles == 0 || lds > 80 * 1024) return false;   // k = 0: nothing to load
   // waves a row tile: the fewest tiles, and a joining of sums that costs about one, for the busiest CU
   W4Walk w = {0, x_ld};
   int64_t least = -1;

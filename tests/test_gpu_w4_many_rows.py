@@ -97,3 +97,18 @@ def test_strides_of_an_odd_number_of_rows():
         close(out.t, y, w4_tolerance(y, size, 260, "f16"), "y")
 
 
+
+
+def test_no_columns_and_many_rows():
+    """k = 0 has nothing to load, and sums of nothing."""
+    plan = nm.nm_w4_plan_init(17000, 2, 0, group=0, sparse=True, ldx=16)
+    y = torch.full((2, 17000), 7.0, dtype=torch.float16, device="cuda")
+    nm.nm_w4_matvec(plan, plan.empty_packed(), torch.zeros((2, 0), dtype=torch.float16, device="cuda"), y)
+    torch.cuda.synchronize()
+    assert (y == 0).all()
+
+
+def test_more_than_64_kilobytes_of_lds():
+    """Eight tokens of 3840 that a block walks with; sixteen that eight waves turn for three row tiles."""
+    w4_check(16400, 8, 3840, 128, "bf16", "16", True, True)
+    w4_check(12288, 16, 2560, 128, "f16", "16", True, False)
