@@ -15,13 +15,11 @@
 // are summed by the matrix unit in fp32 (int32 for 8-bit x) and the group's
 // scale is applied to that sum in fp32, so a code costs only its unpacking.
 //
-// Two kernels. w4_kernel: a block takes R tiles of 16 rows; its waves share out
-// the tiles of k, two of them in registers at a time, with their piece of x, and
-// add their sums through LDS in wave order (the order of a sum depends on the
-// shape alone). w4_walk_kernel (2:4 weights, 16-bit x, many rows): x lies in LDS,
-// and blocks walk over the row tiles. The matrix instruction's 16 columns hold
-// the tokens; columns past n repeat the last token's address (the same cache
-// line) and are not stored. Up to NT * 16 tokens share one pass over the weights.
+// A block takes R tiles of 16 rows; its waves share out the tiles of k, two of them in
+// registers at a time, with their piece of x, and add their sums through LDS in wave
+// order (the order of a sum depends on the shape alone). The matrix instruction's 16
+// columns hold the tokens; columns past n repeat the last token's address (the same
+// cache line) and are not stored. Up to NT * 16 tokens share one pass over the weights.
 //
 // Lane layouts (l % 16 = row or column, q = l / 16; accumulator D[4q + r][l % 16]):
 //  dense 16-bit 16x16x32: k = 8q ..; dense int8 16x16x64: k = 16q ..
@@ -172,27 +170,32 @@ __device__ __forceinline__ void w4_store(const W4Args& A, floatx4 v, int col, in
   }
 }
 
-// What one tile of k of R row tiles needs from memory; x with it for up to 16 tokens.
-template <int XT, bool SPARSE, int F, int NT, int R, bool XL> struct W4Tile {
+// What one tile of k of R row tiles needs from memory besides scales; x with it for up to 16 tokens.
+template <int XT, bool SPARSE, int NT, int R, bool XL> struct W4Tile {
   u32x4 c[R];
   u32x2 mt[R];
-  u32x2 sc[R][F];
-  uint32_t z[R][F];
   std::conditional_t<XL, u32x4[(XT == DT_I8 ? 2 : 4) * (SPARSE ? 2 : 1)],
                      typename W4Type<XT>::template b<SPARSE>[NT == 1 ? (XT == DT_I8 ? 2 : 4) : 1]> x;
 };
 
+// A wave fetches the scales and zero points of 16 applications of a row tile at a time, into its own LDS.
+constexpr int W4_ENTRIES = 16;
+constexpr int W4_SCALE_LDS = W4_ENTRIES * (32 + 16);
+
 // Bytes of LDS in which a wave turns a tile of x, 16 tokens 16 bytes apart in their banks.
 constexpr int w4_turn(int tile_bytes) { return 16 * (tile_bytes + 16); }
 
-// What bounds it: the loads of x. They come from the L1 cache, 1 KB (2:4: 2 KB) a
-// matrix instruction against 256 to 512 bytes of codes, so each piece of x serves R row
-// tiles; and R is chosen so that the blocks are whole rounds of the 256 CUs. The matrix
-// instruction's order has neighbouring lanes load from different tokens, a cache line
-// each; with XL they load a token's row along, and the wave turns the tile in LDS.
-// 16384x4096, one f16 token, 8.5 us with R = 4 (34 MB, 4.1 TB/s; 11.1 with R = 1),
-// 16 tokens 9.3 (18.7); 32768x32768, four 8-bit tokens, 87 us (559 MB, 6.4 TB/s;
-// 115 with R = 1). Codes are loaded past the caches' reuse (nontemporal): x stays there.
+// What bounds it: loads other than the codes'. x comes from the L1 cache, 1 KB (2:4:
+// 2 KB) a matrix instruction against 256 to 512 bytes of codes, so each piece of x serves
+// R row tiles; and R is chosen so that the blocks are whole rounds of the 256 CUs. The
+// matrix instruction's order has neighbouring lanes load from different tokens, a
+// cache line each; with XL they load a token's row along, and the wave turns the tile in
+// LDS. Scales come for 16 applications at a time: fetched with each tile, 8 bytes a lane,
+// they cost 32003x4096 (five tokens, two scales a tile) 15.6 us instead of 13.5 (70 MB,
+// 5.2 TB/s). 16384x4096, one f16 token, 8.2 us with R = 4 (34 MB, 4.2 TB/s; 10.3 with
+// R = 1), 16 tokens 8.9 (17.8); 32768x32768, four 8-bit tokens, 87 us (562 MB, 6.5 TB/s;
+// 97 with R = 1); 2:4 22016x4096, one bf16 token, 9.5 us (35 MB, 3.7 TB/s).
+// Codes are loaded past the caches' reuse (nontemporal): x stays there.
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R, bool XL>
 __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   static_assert(!XL || NT == 1, "x is turned for up to 16 tokens");
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   typedef typename W4Type<XT>::template b<SPARSE> b_t;
   constexpr int TB = TK * ESZ;                   // bytes of a token's row in a tile
   constexpr int LPR = TB / 16;                   // lanes that load them
-  typedef W4Tile<XT, SPARSE, F, NT, R, XL> tile_t;
+  typedef W4Tile<XT, SPARSE, NT, R, XL> tile_t;
   extern __shared__ floatx4 red[];
 
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
@@ -257,20 +260,6 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
         asm("" : "+s"(pm));
         T.mt[r] = __builtin_nontemporal_load((gptr8)(pm + (uint32_t)lane * 8));
       }
-#pragma unroll
-      for (int f = 0; f < F; f++) {
-        const uint32_t u = (uint32_t)(t * F + f);
-        // the last tile may reach past the last group (its x is zero there)
-        const uint32_t g = min(__umulhi(2 * u, A.group_magic), (uint32_t)A.groups - 1u);
-        gptr ps = (gptr)A.scales + (rt[r] * A.groups + g) * 32;
-        asm("" : "+s"(ps));
-        T.sc[r][f] = *(gptr8)(ps + (uint32_t)q * 8);
-        if constexpr (ZEROS) {
-          gptr pz = (gptr)A.zeros + (rt[r] * A.groups + g) * 16;
-          asm("" : "+s"(pz));
-          T.z[r][f] = pz[(uint32_t)l16];
-        } else T.z[r][f] = 8;
-      }
     }
     if constexpr (XL) {
 #pragma unroll
@@ -289,7 +278,39 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
 #pragma unroll
     for (int j = 0; j < NT; j++) y[r][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  uint8_t* const turn = (uint8_t*)(red + waves * NT * R * 64) + wave * w4_turn(TB);
+  // Lane 4 e + i: a quarter of the scales of this wave's application e from its tile t
+  // on; those that begin past k are 0, whatever the scale.
+  uint8_t* const own = (uint8_t*)(red + waves * NT * R * 64) + wave * (R * W4_SCALE_LDS);
+  u32x2 sv[R];
+  uint32_t zv[R];
+  bool within = false;
+  auto load_scales = [&](int t) {
+    const uint32_t e = lane >> 2, u = (uint32_t)(t + (int)(e / F) * waves) * F + e % F;
+    const uint32_t g = min(__umulhi(2 * u, A.group_magic), (uint32_t)A.groups - 1u);
+    within = u * (TK / F) < (uint32_t)A.k;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const int64_t at = rt[r] * A.groups + g;
+      sv[r] = *(const u32x2*)((const uint8_t*)A.scales + at * 32 + (lane & 3) * 8);
+      if constexpr (ZEROS) zv[r] = *(const uint32_t*)(A.zeros + at * 16 + (lane & 3) * 4);
+    }
+  };
+  constexpr int CI = W4_ENTRIES / F;             // tiles whose scales come at a time
+  int ci = CI, st = wave;
+  // Before the first tile of each CI: what was fetched goes to LDS, the next is asked for.
+  auto scales_ready = [&]() {
+    if (ci < CI) return;
+    ci = 0;
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      *(u32x2*)(own + r * W4_SCALE_LDS + lane * 8) = within ? sv[r] : u32x2{0, 0};
+      if constexpr (ZEROS) *(uint32_t*)(own + r * W4_SCALE_LDS + W4_ENTRIES * 32 + lane * 4) = zv[r];
+    }
+    st += CI * waves;
+    if (st < A.tiles) load_scales(st);
+  };
+
+  uint8_t* const turn = (uint8_t*)(red + waves * NT * R * 64) + waves * (R * W4_SCALE_LDS) + wave * w4_turn(TB);
   auto compute = [&](const tile_t& T, int t, bool whole) {
     if constexpr (XL) {
 #pragma unroll
@@ -298,12 +319,13 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
     }
 #pragma unroll
     for (int f = 0; f < F; f++) {
-      if (!whole && t * TK + f * SF * KS >= A.k) break;
       W4Zero<XT, ZEROS> zp[R];
       acc_t acc[R][NT];
+      u32x2 sc[R];
 #pragma unroll
       for (int r = 0; r < R; r++) {
-        zp[r].set(T.z[r][f]);
+        sc[r] = *(const u32x2*)(own + r * W4_SCALE_LDS + (ci * F + f) * 32 + q * 8);
+        zp[r].set(ZEROS ? own[r * W4_SCALE_LDS + W4_ENTRIES * 32 + (ci * F + f) * 16 + l16] : 8u);
 #pragma unroll
         for (int j = 0; j < NT; j++) acc[r][j] = acc_t{0, 0, 0, 0};
       }
@@ -338,26 +360,30 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
       for (int r = 0; r < R; r++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float sc = from_bits16<YB ? DT_BF16 : DT_F16>((uint16_t)(T.sc[r][f][e / 2] >> (16 * (e % 2))));
+          const float s1 = from_bits16<YB ? DT_BF16 : DT_F16>((uint16_t)(sc[r][e / 2] >> (16 * (e % 2))));
 #pragma unroll
-          for (int j = 0; j < NT; j++) y[r][j][e] = __builtin_fmaf(sc, (float)acc[r][j][e], y[r][j][e]);
+          for (int j = 0; j < NT; j++) y[r][j][e] = __builtin_fmaf(s1, (float)acc[r][j][e], y[r][j][e]);
         }
     }
+    ci++;
   };
 
   // Two tiles in turn, the next one's loads behind the present one's products.
   // Every path into a product has the same loads behind it, or the wait for
   // them would be a wait for all.
   const int full = A.k / TK;      // tiles that lie within k whole
+  if (wave < A.tiles) load_scales(wave);
   if (wave < full) {
     int t = wave;
     tile_t T0, T1;
     load(T0, t, true);
     for (;;) {
+      scales_ready();
       t += waves;
       if (t >= full) { compute(T0, t - waves, true); break; }
       load(T1, t, true);
       compute(T0, t - waves, true);
+      scales_ready();
       t += waves;
       if (t >= full) { compute(T1, t - waves, true); break; }
       load(T0, t, true);
@@ -367,6 +393,7 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   if (full < A.tiles && full % waves == wave) {
     tile_t T;
     load(T, full, false);
+    scales_ready();
     compute(T, full, false);
   }
 
@@ -382,214 +409,18 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   }
 }
 
-// ---------------------------------------------------------------- x in LDS
-
-constexpr int W4_ENTRIES = 16;                     // scale applications a wave fetches at a time
-constexpr int W4_SCALE_LDS = W4_ENTRIES * (32 + 16);
-
-struct W4Walk {
-  int ks_log2;   // waves that share the k of a row tile
-  int x_ld;      // bytes between tokens in LDS
-};
-
-constexpr int W4_WALK_WAVES = 8;
-constexpr int W4_WALK_BLOCKS = 512;                // two a CU
-
-// Up to 16 tokens in LDS, zero past k, so that no tile of W is a special case. Each block
-// takes 8 >> ks_log2 row tiles at a time, and 1 << ks_log2 waves share the k of each.
-// What bounds it: the instructions that unpack the codes, together with the start
-// (x has to be in LDS before the first product). 22016x4096 2:4, bf16, one token:
-// 8.9 us, 35 MB at 3.9 TB/s (w4_kernel 11.2; with loads alone, 7.0).
-template <int XT, bool YB, bool SPARSE, bool ZEROS, int F>
-__global__ void __launch_bounds__(64 * W4_WALK_WAVES) w4_walk_kernel(W4Args A, W4Walk P) {
-  constexpr int ESZ = XT == DT_I8 ? 1 : 2;
-  constexpr int S = XT == DT_I8 ? 2 : 4;         // matrix instructions along a tile
-  constexpr int SF = S / F;                      // of them, between two scales
-  constexpr int TK = SPARSE ? 256 : 128;         // k per tile
-  constexpr int KS = TK / S;
-  constexpr int CI = W4_ENTRIES / F;             // tiles whose scales come at a time
-  typedef typename W4Type<XT>::acc acc_t;
-  typedef typename W4Type<XT>::template b<SPARSE> b_t;
-  struct Item { u32x4 c; u32x2 mt; };
-  extern __shared__ floatx4 lds[];
-
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, q = lane >> 4;
-  floatx4* const red = lds;
-  uint8_t* const own = (uint8_t*)(lds + waves * 64) + wave * W4_SCALE_LDS;   // this wave's scales and zero points
-  uint8_t* const xs = (uint8_t*)(lds + waves * 64) + waves * W4_SCALE_LDS;
-
-  const int ks = 1 << P.ks_log2, slice = wave & (ks - 1), per = waves >> P.ks_log2;
-  const int step = gridDim.x * per;              // row tiles in a pass
-  int base = blockIdx.x * per, rt = base + (wave >> P.ks_log2);
-
-  // Row tiles past the last: that one again, its result not stored.
-  auto load = [&](Item& T, int row_tile, int t) {
-    const int64_t at = (int64_t)min(row_tile, A.row_tiles - 1) * A.tiles + t;
-    gptr pc = (gptr)A.codes + at * 1024;
-    asm("" : "+s"(pc));
-    T.c = __builtin_nontemporal_load((gptr16)(pc + (uint32_t)lane * 16));
-    if constexpr (SPARSE) {
-      gptr pm = (gptr)A.meta + at * 512;
-      asm("" : "+s"(pm));
-      T.mt = __builtin_nontemporal_load((gptr8)(pm + (uint32_t)lane * 8));
-    }
-  };
-  // lane 4 e + i: a quarter of the scales of this wave's application e from its tile t on;
-  // returns whether that application begins before k (what lies past it meets no scale)
-  auto load_scales = [&](u32x2& sc, uint32_t& zp, int row_tile, int t) -> bool {
-    const int64_t r = min(row_tile, A.row_tiles - 1);
-    const uint32_t e = lane >> 2, u = (t + (e / F << P.ks_log2)) * F + e % F;
-    const int64_t g = r * A.groups + min(__umulhi(2 * u, A.group_magic), (uint32_t)A.groups - 1u);
-    sc = *(const u32x2*)((const uint8_t*)A.scales + g * 32 + (lane & 3) * 8);
-    if constexpr (ZEROS) zp = *(const uint32_t*)(A.zeros + g * 16 + (lane & 3) * 4);
-    return u * (TK / F) < (uint32_t)A.k;
-  };
-
-  // x to LDS, 1 KB a wave at a time, eight of them on their way
-  const int row_bytes = A.tiles * TK * ESZ, kb = A.k * ESZ, row_kb = (row_bytes + 1023) & ~1023;
-  int xrow = 0, xc = wave * 1024, xat[8];
-  u32x4 xv[8];
-  auto x_load = [&]() {
-#pragma unroll
-    for (int u = 0; u < 8; u++) {
-      while (xc >= row_kb && xrow < A.n) { xc -= row_kb; xrow++; }
-      const int b = xc + lane * 16;
-      xat[u] = xrow < A.n && b < row_bytes ? xrow * P.x_ld + b : -1;
-      xv[u] = u32x4{0, 0, 0, 0};
-      if (xat[u] >= 0) {
-        const uint8_t* p = A.x + (int64_t)xrow * A.ldx * ESZ + b;
-        if (b + 16 <= kb) xv[u] = *(const u32x4*)p;
-        else
-          for (int e = 0; e < kb - b; e++) xv[u][e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
-      }
-      xc += waves * 1024;
-    }
-  };
-  auto x_store = [&]() {
-#pragma unroll
-    for (int u = 0; u < 8; u++)
-      if (xat[u] >= 0) *(u32x4*)(xs + xat[u]) = xv[u];
-  };
-
-  const uint8_t* const xl = xs + min(l16, A.n - 1) * P.x_ld + q * 16;
-  // tile t; i: its place among those whose scales are in LDS
-  auto compute = [&](const Item& T, int t, int i, floatx4& y) {
-    const uint8_t* const xt = xl + t * (TK * ESZ);
-    const uint8_t* const st = own + i * (F * 32) + q * 8;
-    const uint8_t* const zt = own + W4_ENTRIES * 32 + i * (F * 16) + l16;
-#pragma unroll
-    for (int f = 0; f < F; f++) {
-      const u32x2 sc = *(const u32x2*)(st + f * 32);
-      W4Zero<XT, ZEROS> zp;
-      zp.set(ZEROS ? zt[f * 16] : 8u);
-      acc_t acc = acc_t{0, 0, 0, 0};
-#pragma unroll
-      for (int h = 0; h < SF; h++) {
-        const int s = f * SF + h;
-        uint32_t w[2];
-        if constexpr (ESZ == 2) w[0] = T.c[s];
-        else { w[0] = T.c[2 * s]; w[1] = T.c[2 * s + 1]; }
-        const typename W4Type<XT>::a a = zp.unpack(w);
-        int idx = 0;
-        if constexpr (SPARSE) idx = ESZ == 2 ? (int)(T.mt[s / 2] >> (16 * (s % 2))) : (int)T.mt[s];
-        const u32x4 b0 = *(const u32x4*)(xt + s * KS * ESZ);
-        b_t b;
-        if constexpr (SPARSE) {
-          const u32x4 b1 = *(const u32x4*)(xt + (s * KS + KS / 2) * ESZ);
-          b = __builtin_bit_cast(b_t, __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else b = __builtin_bit_cast(b_t, b0);
-        acc = w4_mma<XT, SPARSE>(a, b, acc, idx);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; e++)
-        y[e] = __builtin_fmaf(from_bits16<YB ? DT_BF16 : DT_F16>((uint16_t)(sc[e / 2] >> (16 * (e % 2)))), (float)acc[e], y[e]);
-    }
-  };
-
-  auto sync = [&]() {   // of LDS alone: loads from memory stay on their way
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-
-  // the waves' sums of a pass, added in the order of the slices
-  auto finish = [&](const floatx4& y) {
-    red[wave * 64 + lane] = y;
-    sync();
-    if (slice == 0) {
-      floatx4 v = y;
-#pragma unroll 4
-      for (int w = 1; w < ks; w++) v += red[(wave + w) * 64 + lane];
-      w4_store<XT, YB, ZEROS>(A, v, l16, (int64_t)rt * 16 + 4 * q);
-    }
-    sync();
-  };
-
-  x_load();
-  Item T0, T1;
-  u32x2 sv;
-  uint32_t zv = 0;
-  int lt = slice, lrt = rt, ct = slice, st = slice, srt = rt, ci = CI;
-  auto fetch = [&](Item& to) {
-    load(to, lrt, lt);
-    lt += ks;
-    if (lt >= A.tiles) { lt = slice; lrt += step; }
-    __builtin_amdgcn_sched_barrier(0);           // on its way before the products that follow
-  };
-  bool within = load_scales(sv, zv, srt, st);
-  fetch(T0);
-  for (;;) {
-    x_store();
-    if (xrow >= A.n) break;
-    x_load();
-  }
-  sync();
-
-  floatx4 y = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  // One tile, the next one's loads before it. The scales that follow are asked
-  // for before those, or the wait for this tile would be one for the next as well.
-  auto turn = [&](Item& cur, Item& next) {
-    if (ci == CI) {
-      *(u32x2*)(own + lane * 8) = within ? sv : u32x2{0, 0};
-      if constexpr (ZEROS) *(uint32_t*)(own + W4_ENTRIES * 32 + lane * 4) = zv;
-      st += CI << P.ks_log2;
-      if (st >= A.tiles) { st = slice; srt += step; }
-      within = load_scales(sv, zv, srt, st);
-      ci = 0;
-    }
-    fetch(next);
-    compute(cur, ct, ci, y);
-    ci++;
-    ct += ks;
-    if (ct >= A.tiles) {
-      if (base < A.row_tiles) finish(y);
-      y = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-      base += step;
-      rt += step;
-      ct = slice;
-      ci = CI;
-    }
-  };
-  do {
-    turn(T0, T1);
-    turn(T1, T0);
-  } while (base < A.row_tiles);
-}
-
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R, bool XL>
 hipError_t w4_go(const W4Args& a, int waves, hipStream_t s) {
   constexpr int TB = (SPARSE ? 256 : 128) * (XT == DT_I8 ? 1 : 2);
   hipLaunchKernelGGL((w4_kernel<XT, YB, SPARSE, ZEROS, F, NT, R, XL>),
                      dim3((unsigned)((a.row_tiles + R - 1) / R), (unsigned)((a.n + 16 * NT - 1) / (16 * NT))),
-                     dim3(64 * waves), (size_t)waves * (NT * R * 1024 + (XL ? w4_turn(TB) : 0)), s, a);
+                     dim3(64 * waves), (size_t)waves * (R * (NT * 1024 + W4_SCALE_LDS) + (XL ? w4_turn(TB) : 0)), s, a);
   return hipGetLastError();
 }
 
 // Row tiles a block: the fewest row tiles for the busiest of 256 CUs, and among
-// equals the most a block, which shares the loads of x (12288x4096, one f16 token: 9.2,
-// 8.6, 7.3 and 7.9 us with 1, 2, 3 and 4).
+// equals the most a block, which shares the loads of x (12288x4096, one f16 token: 8.3,
+// 7.8, 6.7 and 7.2 us with 1, 2, 3 and 4).
 inline int w4_rows(const W4Args& a, int nt, int most) {
   const int64_t cols = (a.n + 16 * nt - 1) / (16 * nt);
   int best = 1;
@@ -601,8 +432,8 @@ inline int w4_rows(const W4Args& a, int nt, int most) {
   return best;
 }
 
-// Waves a block: 8 where a CU has one block, 4 where it has several (12288x4096: 7.3 and
-// 7.5 us; 32003x4096: 17.0 and 15.6), at most one a tile of k.
+// Waves a block: 8 where a CU has one block, 4 where it has several (12288x4096: 6.7 and
+// 7.3 us; 32003x4096: 15.1 and 13.7), at most one a tile of k.
 inline int w4_waves(const W4Args& a, int nt, int r) {
   const int64_t blocks = (int64_t)((a.row_tiles + r - 1) / r) * ((a.n + 16 * nt - 1) / (16 * nt));
   int w = blocks <= 256 ? 8 : 4;
@@ -611,8 +442,8 @@ inline int w4_waves(const W4Args& a, int nt, int r) {
 }
 
 // More than four tokens have x turned, where fewer than four row tiles share its loads
-// (2:4 4096x11008, sixteen 8-bit tokens: 7.2 us, 8.8 without; four tokens 6.9 and 6.9;
-// 16384x4096, sixteen f16 tokens: 9.0 and 8.9).
+// (2:4 4096x11008, sixteen 8-bit tokens: 7.2 us, 8.6 without; four tokens 6.7 and 6.5;
+// 16384x4096, sixteen f16 tokens: 9.2 and 8.9).
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R>
 hipError_t w4_try(const W4Args& a, int r, hipStream_t s) {
   if constexpr (R > 1) {
@@ -624,34 +455,8 @@ hipError_t w4_try(const W4Args& a, int r, hipStream_t s) {
   return w4_go<XT, YB, SPARSE, ZEROS, F, NT, R, false>(a, w4_waves(a, NT, R), s);
 }
 
-// The walk: where w4_kernel would hold 32 registers of x a tile, twice, and a CU gets
-// more than four row tiles (22016x4096 2:4: 8.9 against 11.2 us; 12288x4096: 7.7
-// against 7.0), as long as two blocks' x fit a CU's LDS.
-template <int XT, bool YB, bool ZEROS, int F>
-bool w4_walk(const W4Args& a, hipStream_t s, hipError_t& err) {
-  const int x_ld = (a.tiles * 512 + 255) / 256 * 256 + 16;   // 16 bytes on: the tokens of a read lie in different banks
-  const size_t lds = (size_t)W4_WALK_WAVES * (1024 + W4_SCALE_LDS) + (size_t)a.n * x_ld;
-  if (a.n > 16 || a.row_tiles <= 1024 || a.tiles == 0 || lds > 80 * 1024) return false;   // k = 0: nothing to load
-  // waves a row tile: the fewest tiles, and a joining of sums that costs about one, for the busiest CU
-  W4Walk w = {0, x_ld};
-  int64_t least = -1;
-  for (int k = 0; (1 << k) <= W4_WALK_WAVES && (1 << k) <= a.tiles; k++) {
-    const int64_t per = W4_WALK_WAVES >> k, pass = W4_WALK_BLOCKS * per, half = W4_WALK_BLOCKS / 2 * per;
-    const int64_t passes = (a.row_tiles + pass - 1) / pass + (a.row_tiles > half ? (a.row_tiles - half + pass - 1) / pass : 0);
-    const int64_t load = passes * (((a.tiles + (1 << k) - 1) >> k) + 1);
-    if (least < 0 || load < least) { least = load; w.ks_log2 = k; }
-  }
-  hipLaunchKernelGGL((w4_walk_kernel<XT, YB, true, ZEROS, F>), dim3(W4_WALK_BLOCKS), dim3(64 * W4_WALK_WAVES), lds, s, a, w);
-  err = hipGetLastError();
-  return true;
-}
-
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F>
 hipError_t w4_cols(const W4Args& a, hipStream_t s) {
-  if constexpr (SPARSE && XT != DT_I8) {
-    hipError_t e;
-    if (w4_walk<XT, YB, ZEROS, F>(a, s, e)) return e;
-  }
   if (a.n <= 16) return w4_try<XT, YB, SPARSE, ZEROS, F, 1, 4>(a, w4_rows(a, 1, 4), s);
   if (a.n <= 32) return w4_try<XT, YB, SPARSE, ZEROS, F, 2, 2>(a, w4_rows(a, 2, 2), s);
   return w4_try<XT, YB, SPARSE, ZEROS, F, 3, 2>(a, w4_rows(a, 3, 2), s);

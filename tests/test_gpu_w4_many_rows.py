@@ -1,6 +1,5 @@
-"""The 4-bit product where blocks take several row tiles, and where they walk over
-them (2:4 weights with 16-bit x and more than 16384 rows), against the same
-64-bit computation and with the same tolerances as tests/test_gpu_layer_ops.py."""
+"""The 4-bit product where blocks take several row tiles, against the same 64-bit
+computation and with the same tolerances as tests/test_gpu_layer_ops.py."""
 import pytest
 import torch
 
@@ -30,18 +29,18 @@ def test_token_counts(n, x, sparse):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("k", [4, 252, 256, 516, 2048, 4100])
-def test_walk_over_the_rows(dtype, zeros, k):
+def test_many_sparse_rows(dtype, zeros, k):
     for i, (group, n) in enumerate(((0, 1), (64, 3), (128, 16), (192, 8), (256, 2), (512, 1))):
         w4_check((16400, 17003, 24576)[i % 3], n, k, group, dtype, "16", True, zeros, pad=16 * (i % 2), seed=i)
 
 
-def test_walk_with_k_in_more_pieces_than_scales_at_a_time():
-    """Rows of 33 tiles and more: a wave fetches its scales several times a row tile."""
+def test_k_in_more_pieces_than_scales_at_a_time():
+    """Rows of 33 tiles and more: a wave fetches its scales several times."""
     w4_check(16400, 1, 16388, 64, "f16", "16", True, True)
     w4_check(16400, 2, 9000, 128, "bf16", "16", True, False)
 
 
-def test_walk_keeps_tokens_apart():
+def test_many_rows_keep_tokens_apart():
     """A token with a NaN leaves the other tokens' results bit for bit; so does what lies past k."""
     s = w4_inputs(17000, 6, 516, 128, "f16", "16", True, True, 2)
     a = w4_run(s, 17000, 6, 516, 128, "f16", "16")
@@ -52,7 +51,7 @@ def test_walk_keeps_tokens_apart():
     assert torch.equal(torch.isnan(b[5]).cpu(), meets)
 
 
-def test_walk_repeats_bit_for_bit():
+def test_many_rows_repeat_bit_for_bit():
     s = w4_inputs(22016, 4, 1028, 128, "bf16", "16", True, False, 3)
     plan = w4_plan(s, 22016, 4, 1028, 128, "bf16", "16")
     packed, x = w4_pack(plan, s), strided(s["x"], plan._strides[0], 0)[0]
@@ -109,6 +108,6 @@ def test_no_columns_and_many_rows():
 
 
 def test_more_than_64_kilobytes_of_lds():
-    """Eight tokens of 3840 that a block walks with; sixteen that eight waves turn for three row tiles."""
+    """Sixteen tokens that eight waves turn for three row tiles."""
     w4_check(16400, 8, 3840, 128, "bf16", "16", True, True)
     w4_check(12288, 16, 2560, 128, "f16", "16", True, False)
