@@ -340,8 +340,8 @@ nm_status_t nm_swiglu(nm_rows_plan_t plan, const void* dX, const float* d_row_sc
  * row-major (y is nm_spmm's D with order_cd = NM_COL_MAJOR). The kernel is made
  * for few tokens: up to 48 share one pass over the weights.
  * x is of type_y, or NM_I8 with one x_scale a token (1 where x is of type_y).
- * Products of a group are summed in fp32 (exactly in int32 for NM_I8), groups
- * in fp32, rounded once to type_y. */
+ * Up to 128 products of a group are summed in fp32 (exactly in int32 for NM_I8),
+ * these sums times the scale in fp32, rounded once to type_y. */
 typedef struct {
   int64_t m, n, k;          /* m <= 2^24, n <= 2^20, k <= 2^20; sparse: k % 4 == 0 */
   int64_t group;            /* k per scale; 0: one scale a row. Otherwise a multiple of 32 (16-bit x) or 64
