@@ -185,6 +185,15 @@ constexpr int W4_SCALE_LDS = W4_ENTRIES * (32 + 16);
 // Bytes of LDS in which a wave turns a tile of x, 16 tokens 16 bytes apart in their banks.
 constexpr int w4_turn(int tile_bytes) { return 16 * (tile_bytes + 16); }
 
+// Lanes of a wave read what its other lanes wrote to LDS, and write over it once all
+// have read. A wave's LDS operations are carried out in their order, so this emits no
+// instruction; it keeps the compiler from moving them past each other.
+__device__ __forceinline__ void w4_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // What bounds it: loads other than the codes'. x comes from the L1 cache, 1 KB (2:4:
 // 2 KB) a matrix instruction against 256 to 512 bytes of codes, so each piece of x serves
 // R row tiles; and R is chosen so that the blocks are whole rounds of the 256 CUs. The
@@ -301,11 +310,13 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   auto scales_ready = [&]() {
     if (ci < CI) return;
     ci = 0;
+    w4_lds_order();
 #pragma unroll
     for (int r = 0; r < R; r++) {
       *(u32x2*)(own + r * W4_SCALE_LDS + lane * 8) = within ? sv[r] : u32x2{0, 0};
       if constexpr (ZEROS) *(uint32_t*)(own + r * W4_SCALE_LDS + W4_ENTRIES * 32 + lane * 4) = zv[r];
     }
+    w4_lds_order();
     st += CI * waves;
     if (st < A.tiles) load_scales(st);
   };
@@ -313,9 +324,11 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
   uint8_t* const turn = (uint8_t*)(red + waves * NT * R * 64) + waves * (R * W4_SCALE_LDS) + wave * w4_turn(TB);
   auto compute = [&](const tile_t& T, int t, bool whole) {
     if constexpr (XL) {
+      w4_lds_order();
 #pragma unroll
       for (int i = 0; i < 16 * TB / 1024; i++)
         *(u32x4*)(turn + (i * (64 / LPR) + lane / LPR) * (TB + 16) + lane % LPR * 16) = T.x[i];
+      w4_lds_order();
     }
 #pragma unroll
     for (int f = 0; f < F; f++) {
