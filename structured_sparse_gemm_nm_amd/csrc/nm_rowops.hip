@@ -38,6 +38,8 @@ constexpr int ROW_MOST = 1024;    // threads a row
 // 16 bytes at an address that may be off the 16-byte grid (the up half of a
 // row starts at any column)
 struct __attribute__((packed, aligned(2))) U16x8 { u32x4 v; };
+// 8 bytes anywhere: 8-bit rows of fewer than 16 columns start at any byte
+struct __attribute__((packed, aligned(1))) U8x8 { u32x2 v; };
 
 // ROW_V columns of a row as they lie in memory. The loads of a row are all on
 // their way before the first is used, so they are free of branches: a thread past
@@ -129,7 +131,7 @@ __device__ __forceinline__ void store8(uint8_t* row, int64_t c, int64_t cols, co
     o[i] = t != t ? 0u : (uint32_t)(int)__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) & 0xFFu;
   }
   if (!TAIL || c + ROW_V <= cols) {
-    *(u32x2*)(row + c) = u32x2{o[0] | o[1] << 8 | o[2] << 16 | o[3] << 24, o[4] | o[5] << 8 | o[6] << 16 | o[7] << 24};
+    ((U8x8*)(row + c))->v = u32x2{o[0] | o[1] << 8 | o[2] << 16 | o[3] << 24, o[4] | o[5] << 8 | o[6] << 16 | o[7] << 24};
   } else {
 #pragma unroll
     for (int i = 0; i < ROW_V; i++)
