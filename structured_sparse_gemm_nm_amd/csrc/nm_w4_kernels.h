@@ -62,7 +62,11 @@ template <> struct W4Type<DT_I8> {
 //       half of a byte is 16 (q - 8). With zero points 128 + q - z never borrows
 //       from its neighbour byte, and flipping the top bit leaves q - z.
 //  bf16: there is no packed bf16 arithmetic; the bytes of int8 are converted to
-//       fp32, whose upper half is the value's bf16.
+//       fp32, whose upper half is the value's bf16. Without zero points the
+//       conversion of a 4-bit two's complement nibble gives (q - 8) / 16, and the
+//       16 is multiplied into the result: a sum that fp32 holds cannot overflow on
+//       the way, and products of bf16 values by multiples of 1/16 down to fp32's
+//       smallest are exact.
 template <int XT, bool ZEROS> struct W4Zero;
 
 template <bool ZEROS> struct W4Zero<DT_F16, ZEROS> {
@@ -105,8 +109,8 @@ template <bool ZEROS> struct W4Bytes {
   }
 };
 
-template <bool ZEROS> struct W4Zero<DT_BF16, ZEROS> {
-  W4Bytes<ZEROS> b;
+template <> struct W4Zero<DT_BF16, true> {
+  W4Bytes<true> b;
   __device__ __forceinline__ void set(uint32_t z) { b.set(z); }
   __device__ __forceinline__ bf16x8_t unpack(const uint32_t* w) const {
     uint32_t h[2];
@@ -117,6 +121,22 @@ template <bool ZEROS> struct W4Zero<DT_BF16, ZEROS> {
       const uint32_t v = h[i / 2] >> (16 * (i % 2));
       r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, (float)(int8_t)(v >> 8)),
                                    __builtin_bit_cast(uint32_t, (float)(int8_t)v), 0x07060302u);
+    }
+    return __builtin_bit_cast(bf16x8_t, r);
+  }
+};
+
+template <> struct W4Zero<DT_BF16, false> {
+  __device__ __forceinline__ void set(uint32_t) {}
+  __device__ __forceinline__ bf16x8_t unpack(const uint32_t* w) const {
+    uint32_t h[2] = {w[0], w[0] >> 4};
+    asm("" : "+v"(h[1]));   // shifted once, its bytes picked by the conversions
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t v = h[i / 2] >> (16 * (i % 2));
+      r[i] = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_off_f32_i4((int)(v >> 8 & 0xFF))),
+                                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_off_f32_i4((int)(v & 0xFF))), 0x07060302u);
     }
     return __builtin_bit_cast(bf16x8_t, r);
   }
@@ -156,7 +176,7 @@ template <int XT, bool YB, bool ZEROS>
 __device__ __forceinline__ void w4_store(const W4Args& A, floatx4 v, int col, int64_t row) {
   if (col >= A.n || row >= A.m) return;
   if constexpr (XT == DT_I8) v *= A.x_scale[col];
-  if constexpr (XT != DT_F16 && !ZEROS) v *= 0.0625f;    // these codes are held times 16
+  if constexpr (XT == DT_BF16 && !ZEROS) v *= 16.0f;     // these codes are held as sixteenths
   uint16_t o[4];
 #pragma unroll
   for (int e = 0; e < 4; e++) o[e] = to_bits16<YB ? DT_BF16 : DT_F16>(v[e]);
@@ -373,7 +393,8 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
       for (int r = 0; r < R; r++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float s1 = from_bits16<YB ? DT_BF16 : DT_F16>((uint16_t)(sc[r][e / 2] >> (16 * (e % 2))));
+          float s1 = from_bits16<YB ? DT_BF16 : DT_F16>((uint16_t)(sc[r][e / 2] >> (16 * (e % 2))));
+          if constexpr (XT == DT_I8 && !ZEROS) s1 *= 0.0625f;   // these codes are held times 16
 #pragma unroll
           for (int j = 0; j < NT; j++) y[r][j][e] = __builtin_fmaf(s1, (float)acc[r][j][e], y[r][j][e]);
         }
