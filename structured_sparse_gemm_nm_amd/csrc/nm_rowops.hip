@@ -94,13 +94,14 @@ __device__ __forceinline__ void part32(T (&o)[ROW_V], const T* row, int64_t c, i
   for (int i = 0; i < ROW_V; i++) o[i] = c + i < cols ? row[c + i] : (T)0;
 }
 
-// silu(g) * u. exp of -|g| neither overflows nor divides by a large number; as
-// the square of exp(-|g| / 2) it keeps the subnormal results that the
-// exponential instruction flushes, which bf16 rows can hold.
+// silu(g) * u. For g < 0, with p = exp(-|g| / 2), as (g p / (1 + p p)) (p u): the
+// first factor stays under 1 and above fp32's smallest values where exp(-|g|) is
+// past them, so a large u meets all of its bits. p is the square of exp(-|g| / 4):
+// the exponential instruction flushes subnormal results.
 __device__ __forceinline__ float gated(float g, float u) {
-  const float half = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * 0.72134752044448f), e = half * half;
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  return g * (g < 0.0f ? e * r : r) * u;
+  const float root = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * 0.36067376022224f), p = root * root;
+  const float r = __builtin_amdgcn_rcpf(__builtin_fmaf(p, p, 1.0f)), s = g < 0.0f ? p : 1.0f;
+  return g * (s * r) * (s * u);
 }
 
 template <int IO, bool TAIL>
