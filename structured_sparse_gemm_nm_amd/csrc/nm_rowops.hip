@@ -330,11 +330,17 @@ __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
     for (int p = 0; p < C; p++)
       if (first + p * stride < A.cols) make(v[p], P[p], first + p * stride, sum, top, true);
   } else {
+    // Up to 2^17 pieces a thread: a chain of 2^20 equal squares in fp32 is off by up to 0.8 %,
+    // so pieces join in 64 bits (2 x 2^24 columns: 2868 us, 2854 with one fp32 chain)
+    double total = 0.0;
     for (int64_t c = first; c < A.cols; c += stride) {
       piece_t P;
+      float part = 0.0f;
       load(P, c);
-      make(v[0], P, c, sum, top, false);
+      make(v[0], P, c, part, top, false);
+      if constexpr (NORM) total += (double)part;
     }
+    sum = (float)total;
   }
   float f = 1.0f, r = 0.0f;
   bool small = false;
