@@ -118,19 +118,29 @@ class CompressedFeedForward:
         self._plans = {}
 
     def _rows(self, op, n, cols, x):
-        key = (op, n, x.values.dtype)
-        plan = self._plans.get(key)
+        acc = x.values.dtype == torch.int32
+        plan = self._plans.get((op, n, acc))
         if plan is None:
-            plan = self._plans[key] = nm_rows_plan_init(
-                n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype=None if x.row_scale is None else "i32",
-                y_dtype="i8", eps=self.eps)
+            plan = self._plans[op, n, acc] = nm_rows_plan_init(
+                n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype="i32" if acc else None, y_dtype="i8", eps=self.eps)
         return plan
+
+    def _check(self, x):
+        """x is what a plan of the block can be made for."""
+        if x.values.dim() != 2 or x.values.shape[1] != self.hidden:
+            raise ValueError("x must be (tokens x %d), got %s" % (self.hidden, tuple(x.values.shape)))
+        if x.values.dtype not in (self.dtype, torch.int32):
+            raise ValueError("x must be %s or int32 accumulators, got %s" % (self.dtype, x.values.dtype))
+        acc = x.values.dtype == torch.int32
+        if (x.row_scale is not None) != acc or (x.col_scale is not None) != acc:
+            raise ValueError("row_scale and col_scale must be given exactly where x is int32")
 
     def __call__(self, x, residual=None, few=None):
         """x: Rows or a 16-bit tensor (tokens x hidden); residual: 16-bit (tokens x hidden) or None.
         Returns the down product as Rows and the next residual h = x + residual.
         few: which product to take; by default the 4-bit one up to FEW_TOKENS tokens."""
         x = x if isinstance(x, Rows) else Rows(x)
+        self._check(x)
         n, device = x.values.shape[0], x.values.device
         few = n <= FEW_TOKENS if few is None else few
         codes = torch.empty((n, self.hidden), dtype=torch.int8, device=device)

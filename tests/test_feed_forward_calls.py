@@ -1,0 +1,35 @@
+"""Host side of the feed-forward block: what a call refuses before a plan is made, and which plan a call is given."""
+import pytest
+import torch
+
+from structured_sparse_gemm_nm_amd.feed_forward import CompressedFeedForward, Rows
+
+
+def block(dtype=torch.float16, hidden=32, inner=48):
+    """A block without weights: calls reach its checks and its row operators' plans."""
+    ff = CompressedFeedForward.__new__(CompressedFeedForward)
+    ff.hidden, ff.inner, ff.dtype, ff.eps, ff._plans = hidden, inner, dtype, 1e-6, {}
+    return ff
+
+
+X, ACC = torch.zeros((4, 32), dtype=torch.float16), torch.zeros((4, 32), dtype=torch.int32)
+ROW, COL = torch.ones(4), torch.ones(32)
+
+
+@pytest.mark.parametrize("bad", [
+    Rows(ACC), Rows(ACC, ROW), Rows(ACC, None, COL), Rows(X, ROW, COL), Rows(X, None, COL), Rows(X, ROW), X.bfloat16(),
+    X.float(), X[:, :16], X[0], X[None], Rows(ACC[:, :16], ROW, COL[:16]),
+])
+def test_refused_before_a_plan_is_made(bad):
+    ff = block()
+    with pytest.raises(ValueError):
+        ff(bad)
+    assert len(ff._plans) == 0
+
+
+def test_a_plan_follows_the_type_of_the_values():
+    ff = block()
+    for op, cols in (("rmsnorm", 32), ("swiglu", 48)):
+        for values, scales, dtype in ((ACC, (ROW, COL), torch.int32), (X, (), torch.float16), (ACC, (), torch.int32)):
+            plan = ff._rows(op, 4, cols, Rows(values, *scales))
+            assert plan.x_dtype is dtype and plan is ff._rows(op, 4, cols, Rows(values, *scales))
