@@ -36,6 +36,28 @@ _DTYPE_NAMES = {torch.float16: "f16", torch.bfloat16: "bf16"}
 FEW_TOKENS = 96
 
 
+# Plans that a block keeps, of each of its weights and of its row operators: one for each number of tokens
+# and product, the least recently used given up first. They hold host memory only.
+MOST_PLANS = 256
+
+
+class _Plans:
+    def __init__(self):
+        self._kept = {}
+
+    def __len__(self):
+        return len(self._kept)
+
+    def get(self, key, make):
+        plan = self._kept.pop(key, None)
+        if plan is None:
+            plan = make()
+        self._kept[key] = plan                     # the last in the dictionary's order
+        if len(self._kept) > MOST_PLANS:
+            self._kept.pop(next(iter(self._kept)), None)
+        return plan
+
+
 class Rows(NamedTuple):
     """What a product hands on: 16-bit values, or int32 accumulators with a scale a row and a column."""
 
@@ -69,7 +91,7 @@ class _Weight:
         self.few = nm_w4_plan_init(out_f, 1, in_f, group=0, dtype=self.dtype, x_dtype="i8", sparse=True)
         self.packed = self.few.empty_packed(device=w.device)
         nm_w4_pack(self.few, codes[:, 0::2] | codes[:, 1::2] << 4, scale[:, None].contiguous(), self.packed, meta=self.meta)
-        self._plans = {}
+        self._plans = _Plans()
 
     def dense(self):
         """The weight that both products multiply by, in fp32."""
@@ -81,16 +103,14 @@ class _Weight:
 
     def product(self, x, x_scale, few):
         n, device = x.shape[0], x.device
-        plan = self._plans.get((n, few))
         if few:
-            if plan is None:
-                plan = self._plans[n, few] = nm_w4_plan_init(self.out_f, n, self.in_f, group=0, dtype=self.dtype,
-                                                             x_dtype="i8", sparse=True)
+            plan = self._plans.get((n, few), lambda: nm_w4_plan_init(self.out_f, n, self.in_f, group=0, dtype=self.dtype,
+                                                                     x_dtype="i8", sparse=True))
             y = torch.empty((n, self.out_f), dtype=plan.y_dtype, device=device)
             nm_w4_matvec(plan, self.packed, x, y, x_scale=x_scale)
             return Rows(y)
-        if plan is None:
-            plan = self._plans[n, few] = nm_plan_init(self.out_f, n, self.in_f, 2, 4, dtype="i8", op_b="T", order_cd="col")
+        plan = self._plans.get((n, few), lambda: nm_plan_init(self.out_f, n, self.in_f, 2, 4, dtype="i8", op_b="T",
+                                                              order_cd="col"))
         y = torch.empty((n, self.out_f), dtype=torch.int32, device=device)
         nm_spmm(plan, 1.0, self.values, self.meta, x, 0.0, None, y)
         return Rows(y, x_scale, self.scale)
@@ -115,15 +135,12 @@ class CompressedFeedForward:
             raise ValueError("hidden and inner must be positive multiples of 16")
         self.gamma, self.eps, self.dtype = gamma, eps, gamma.dtype
         self.gate_up, self.down = _Weight(gate_up), _Weight(down)
-        self._plans = {}
+        self._plans = _Plans()
 
     def _rows(self, op, n, cols, x):
         acc = x.values.dtype == torch.int32
-        plan = self._plans.get((op, n, acc))
-        if plan is None:
-            plan = self._plans[op, n, acc] = nm_rows_plan_init(
-                n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype="i32" if acc else None, y_dtype="i8", eps=self.eps)
-        return plan
+        return self._plans.get((op, n, acc), lambda: nm_rows_plan_init(
+            n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype="i32" if acc else None, y_dtype="i8", eps=self.eps))
 
     def _check(self, x):
         """x is what a plan of the block can be made for."""

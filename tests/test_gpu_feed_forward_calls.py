@@ -1,8 +1,9 @@
-"""The feed-forward block's calls: a refused call leaves later calls as they were."""
+"""The feed-forward block's calls: a refused call leaves later calls as they were, and plans are kept for the latest
+numbers of tokens only."""
 import pytest
 import torch
 
-from structured_sparse_gemm_nm_amd.feed_forward import Rows
+from structured_sparse_gemm_nm_amd.feed_forward import MOST_PLANS, Rows
 from tests.test_gpu_feed_forward import block, inputs
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,17 @@ def test_a_refused_call_leaves_later_calls_as_they_were(few):
     for good in (x, acc):
         (y, h), (want, hw) = ff(good, r, few=few), other(good, r, few=few)
         assert torch.equal(y.values, want.values) and torch.equal(h, hw)
+
+
+def test_plans_are_kept_for_the_latest_numbers_of_tokens():
+    ff, _, _ = block(32, 48, torch.bfloat16)
+    x, r = inputs(700, 32, torch.bfloat16)
+    first, _ = ff(x[:3], r[:3])
+    for n in range(1, 701):
+        ff(x[:n], r[:n], few=True)
+        if n % 7 == 0:
+            ff(x[:n], r[:n], few=False)
+    for plans in (ff._plans, ff.gate_up._plans, ff.down._plans):
+        assert 0 < len(plans) <= MOST_PLANS
+    again, _ = ff(x[:3], r[:3])
+    assert torch.equal(again.values, first.values)
