@@ -19,7 +19,8 @@ The 8-bit activations of the two are the same; they differ in the 16-bit roundin
 of the few-token products alone.
 
 Features must be multiples of 16. Weights are prepared with torch; every call runs
-in the library's kernels and may be captured into a graph.
+in the library's kernels and may be captured into a graph. There is no backward
+pass: operands that require a gradient are refused while gradients are recorded.
 """
 from typing import NamedTuple, Optional
 
@@ -118,7 +119,8 @@ class _Weight:
 
 class CompressedFeedForward:
     """gamma (hidden), gate_up (2 * inner x hidden: the gate's rows, then the up rows), down (hidden x inner):
-    16-bit GPU tensors of one type. The block keeps their compressed forms only."""
+    16-bit GPU tensors of one type. The block keeps gamma and the weights' compressed forms as constants: a position
+    takes 3/8 byte in 4 bits and 5/8 byte as int8, metadata included, 1 byte together."""
 
     def __init__(self, gamma, gate_up, down, eps=1e-6):
         for name, w in (("gamma", gamma), ("gate_up", gate_up), ("down", down)):
@@ -133,7 +135,7 @@ class CompressedFeedForward:
             raise ValueError("expected gamma (hidden), gate_up (2 * inner x hidden) and down (hidden x inner)")
         if self.hidden % 16 or self.inner % 16 or not self.hidden or not self.inner:
             raise ValueError("hidden and inner must be positive multiples of 16")
-        self.gamma, self.eps, self.dtype = gamma, eps, gamma.dtype
+        self.gamma, self.eps, self.dtype = gamma.detach(), eps, gamma.dtype
         self.gate_up, self.down = _Weight(gate_up), _Weight(down)
         self._plans = _Plans()
 
@@ -142,8 +144,11 @@ class CompressedFeedForward:
         return self._plans.get((op, n, acc), lambda: nm_rows_plan_init(
             n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype="i32" if acc else None, y_dtype="i8", eps=self.eps))
 
-    def _check(self, x):
-        """x is what a plan of the block can be made for."""
+    def _check(self, x, residual):
+        """x is what a plan of the block can be made for, and no operand wants a gradient."""
+        if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (*x, residual)):
+            raise RuntimeError("the block has no backward pass: x and residual must not require a gradient "
+                               "(detach them, or call it under torch.no_grad())")
         if x.values.dim() != 2 or x.values.shape[1] != self.hidden:
             raise ValueError("x must be (tokens x %d), got %s" % (self.hidden, tuple(x.values.shape)))
         if x.values.dtype not in (self.dtype, torch.int32):
@@ -157,7 +162,7 @@ class CompressedFeedForward:
         Returns the down product as Rows and the next residual h = x + residual.
         few: which product to take; by default the 4-bit one up to FEW_TOKENS tokens."""
         x = x if isinstance(x, Rows) else Rows(x)
-        self._check(x)
+        self._check(x, residual)
         n, device = x.values.shape[0], x.values.device
         few = n <= FEW_TOKENS if few is None else few
         codes = torch.empty((n, self.hidden), dtype=torch.int8, device=device)

@@ -9,6 +9,7 @@ def block(dtype=torch.float16, hidden=32, inner=48):
     """A block without weights: calls reach its checks and its row operators' plans."""
     ff = CompressedFeedForward.__new__(CompressedFeedForward)
     ff.hidden, ff.inner, ff.dtype, ff.eps, ff._plans = hidden, inner, dtype, 1e-6, _Plans()
+    ff.gamma = torch.ones(hidden, dtype=dtype)
     return ff
 
 
@@ -51,3 +52,12 @@ def test_a_plan_that_cannot_be_made_is_not_kept():
     with pytest.raises(ZeroDivisionError):
         plans.get(1, lambda: 1 // 0)
     assert len(plans) == 0 and plans.get(1, lambda: 5) == 5 and plans.get(1, lambda: 6) == 5
+
+
+def test_operands_that_want_a_gradient_are_refused():
+    ff, wants = block(), X.clone().requires_grad_()
+    for x, residual in ((wants, None), (X, wants), (Rows(ACC, ROW.clone().requires_grad_(), COL), None), (Rows(wants), X)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            ff(x, residual)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):    # past that check, and on to the next: host tensors
+            ff(x, residual)

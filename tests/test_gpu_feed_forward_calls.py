@@ -1,9 +1,9 @@
-"""The feed-forward block's calls: a refused call leaves later calls as they were, and plans are kept for the latest
-numbers of tokens only."""
+"""The feed-forward block's calls: a refused call leaves later calls as they were, plans are kept for the latest
+numbers of tokens only, and operands that want a gradient are refused."""
 import pytest
 import torch
 
-from structured_sparse_gemm_nm_amd.feed_forward import MOST_PLANS, Rows
+from structured_sparse_gemm_nm_amd.feed_forward import MOST_PLANS, CompressedFeedForward, Rows
 from tests.test_gpu_feed_forward import block, inputs
 
 pytestmark = pytest.mark.gpu
@@ -43,3 +43,24 @@ def test_plans_are_kept_for_the_latest_numbers_of_tokens():
         assert 0 < len(plans) <= MOST_PLANS
     again, _ = ff(x[:3], r[:3])
     assert torch.equal(again.values, first.values)
+
+
+def test_inputs_that_want_a_gradient_are_refused():
+    ff, _, _ = block(64, 96, torch.float16)
+    x, r = inputs(3, 64, torch.float16)
+    want, h = ff(x, r)
+    wants = x.clone().requires_grad_()
+    for a, b in ((wants, r), (x, wants), (Rows(wants), None)):
+        with pytest.raises(RuntimeError, match="gradient"):
+            ff(a, b)
+    with torch.no_grad():
+        y, hh = ff(wants, r)
+    assert torch.equal(y.values, want.values) and torch.equal(hh, h)
+
+
+def test_the_block_keeps_gamma_as_a_constant():
+    _, gate_up, down = block(64, 96, torch.float16)
+    gamma = torch.nn.Parameter(torch.ones(64, dtype=torch.float16, device="cuda"))
+    ff = CompressedFeedForward(gamma, torch.nn.Parameter(gate_up), torch.nn.Parameter(down))
+    y, h = ff(*inputs(3, 64, torch.float16))
+    assert not (ff.gamma.requires_grad or y.values.requires_grad or h.requires_grad)
