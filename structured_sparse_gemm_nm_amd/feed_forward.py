@@ -81,8 +81,11 @@ class _Weight:
         plan = nm_plan_init(out_f, 16, in_f, 2, 4, dtype=self.dtype)
         pruned = torch.empty_like(w)
         nm_prune(plan, w, pruned)
-        amax = pruned.float().abs().amax(1)
-        scale = (amax / 7).clamp_min(torch.finfo(w.dtype).tiny).to(w.dtype)
+        # Below the smallest normal value scales are whole steps of the type: the next one up, or the largest
+        # weight would need more than seven of it. Rows of zeros take one step.
+        info = torch.finfo(w.dtype)
+        scale, step = (pruned.float().abs().amax(1) / 7).double(), info.tiny * info.eps
+        scale = torch.where(scale < info.tiny, (scale / step).ceil().clamp_min(1) * step, scale).to(w.dtype)
         self.scale = scale.float()
         q = (pruned.float() / self.scale[:, None]).round_().clamp_(-8, 7).to(torch.int8)
         plan = nm_plan_init(out_f, 16, in_f, 2, 4, dtype="i8", op_b="T", order_cd="col")

@@ -1,9 +1,9 @@
 """The feed-forward block's calls: a refused call leaves later calls as they were, plans are kept for the latest
-numbers of tokens only, and operands that want a gradient are refused."""
+numbers of tokens only, operands that want a gradient are refused, and small weights keep their values."""
 import pytest
 import torch
 
-from structured_sparse_gemm_nm_amd.feed_forward import MOST_PLANS, CompressedFeedForward, Rows
+from structured_sparse_gemm_nm_amd.feed_forward import MOST_PLANS, CompressedFeedForward, Rows, _Weight
 from tests.test_gpu_feed_forward import block, inputs
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +64,30 @@ def test_the_block_keeps_gamma_as_a_constant():
     ff = CompressedFeedForward(gamma, torch.nn.Parameter(gate_up), torch.nn.Parameter(down))
     y, h = ff(*inputs(3, 64, torch.float16))
     assert not (ff.gamma.requires_grad or y.values.requires_grad or h.requires_grad)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-4, 1e-5, 1e-6, 1e-7])
+def test_small_weights_keep_their_values(size, dtype):
+    """Sixteen steps a row: an error of half a step, a seventh of the largest weight or f16's smallest step."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = (torch.randn(48, 64, generator=g, device="cuda") * size).to(dtype)
+    w[5] = 0
+    packed = _Weight(w)
+    d, o = packed.dense().double(), w.double()
+    kept = d.new_zeros(48, 16, 4).scatter_(2, o.abs().reshape(48, 16, 4).sort(dim=2, descending=True, stable=True).indices[:, :, :2],
+                                           1.0).reshape(48, 64) > 0
+    assert (d[~kept] == 0).all() and (d[5] == 0).all()
+    step = o.abs().amax(1, keepdim=True) / 7
+    least = 2.0 ** -24 if dtype == torch.float16 else 0.0
+    # the scale's own rounding moves the largest weight by 8 half steps of it
+    half = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    bound = (step + least) / 2 + 8 * half * step
+    assert ((d - o).abs() <= bound)[kept].all()
+    # both products multiply by the same integers and scales
+    codes = torch.randint(-127, 128, (4, 64), generator=g, device="cuda", dtype=torch.int32).to(torch.int8)
+    scale = torch.full((4,), 1.0 / size, device="cuda")
+    few, many = packed.product(codes, scale, True), packed.product(codes, scale, False)
+    want = many.values.double() * scale.double()[:, None] * packed.scale.double()
+    sizes = codes.double().abs() @ d.abs().t() * scale.double()[:, None]
+    assert ((few.values.double() - want).abs() <= half * want.abs() + 32 * 2.0 ** -24 * sizes + 2.0 ** -25).all()
