@@ -10,6 +10,7 @@ PyTorch fallback.
 """
 import ctypes
 import os
+import warnings
 
 import torch  # loaded first so the library binds to torch's HIP runtime
 
@@ -55,12 +56,13 @@ class nm_w4_problem_t(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
-_lib = _calls = None
+_lib = _calls = _calls_error = None
 
 
 def lib():
-    """Load libnmsparse.so and its call extension; raises if they have not been built."""
-    global _lib, _calls
+    """Load libnmsparse.so; raises if it has not been built. The call extension is loaded with it where it fits this
+    torch and Python; without it the layer operators' operands are checked in Python."""
+    global _lib, _calls, _calls_error
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libnmsparse.so is not built (run __graft_entry__.build() or "
@@ -68,9 +70,9 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         try:
             from . import _nmcall
+            _calls = _nmcall
         except ImportError as e:
-            raise RuntimeError("_nmcall.so is not built for this torch (run __graft_entry__.build()): %s" % e)
-        _calls = _nmcall
+            _calls_error = str(e)
         P, I32, I64, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         st = ctypes.c_int
         L.nm_plan_init.restype = st; L.nm_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_problem_t)]
@@ -384,9 +386,14 @@ class _LayerPlan:
         self.problem = problem
 
     def _call(self, name, main, *specs):
-        """The entry point with the operands it takes, in its order; main: the operand whose device counts."""
-        fn = ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
-        return _calls.Call(fn, self.handle, main, specs)
+        """The entry point with the operands it takes, in its order; main: the operand whose device counts.
+        None without the call extension."""
+        fn, calls = getattr(lib(), name), _calls
+        if calls is None:
+            warnings.warn("_nmcall.so does not load (run __graft_entry__.build()): each call of the layer operators takes "
+                          "the host 2 to 3 us more. %s" % _calls_error, RuntimeWarning, stacklevel=4)
+            return None
+        return calls.Call(ctypes.cast(fn, ctypes.c_void_p).value, self.handle, main, specs)
 
     def destroy(self):
         self._norm_call = self._gate_call = self._product_call = None

@@ -158,6 +158,8 @@ def _build_call():
            "-Wl,-rpath," + tl]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
+        if os.path.exists(CALL_LIB):
+            os.remove(CALL_LIB)                       # an older library's
         raise RuntimeError("compile failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
     os.replace(tmp, CALL_LIB)
 
@@ -171,7 +173,6 @@ def build(verbose=True):
         call = ex.submit(_build_call)
         objs = list(ex.map(_compile, SOURCES + ["nm_calib.hip"]))
         m0.result()
-        call.result()
     _link(objs[-1:], CAL_LIB, "libnmcal.so")
     objs = objs[:-1]
     tl = torch_lib_dir()
@@ -187,6 +188,7 @@ def build(verbose=True):
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB)
+    call.result()     # last: the library works without the extension
     return LIB
 
 
