@@ -88,7 +88,7 @@ def _m0_check():
 # of B met in a loop variable; the units that hold sparse instructions are
 # compiled with their assembly kept, and one such instruction fails the build.
 SPARSE_SOURCES = ("nm_gemm_f16.hip", "nm_gemm_bf16.hip", "nm_gemm_i8.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip",
-                  "nm_w4_i8.hip", "nm_w4_i8_bf16.hip")
+                  "nm_w4_i8.hip", "nm_w4_i8_bf16.hip", "nm_calib.hip")
 
 
 def check_sparse_operands(asm_path):
