@@ -304,13 +304,16 @@ nm_status_t nm_spmm_workspace_size(nm_plan_t plan, size_t* bytes);
  * product, whose value is x * row_scale[row] * col_scale[column].
  * y is of type_io, or NM_I8: with a = max |v| of the row, y_scale[row] =
  * a * f / 127 and code = v * (127 / a) rounded to nearest even, so that
- * code * y_scale is the value; a row of zeros gives codes and scale zero, a
- * row with a NaN or an infinity a NaN or infinite scale.
- * Everything is computed in fp32 and rounded once. gamma, residual and h are
- * of type_io. */
+ * code * y_scale is the value; a row of zeros gives codes and scale zero (the
+ * norm with eps = 0: f is infinite, the scale NaN, the codes zero), a row with
+ * a NaN or an infinity a NaN or infinite scale.
+ * Everything is computed in fp32 and rounded once; rows of more than 32768
+ * columns (16384 of NM_I32) join the sums of their parts in 64 bits. The norm's
+ * sum of squares has fp32's range: a row whose sum passes 2^128 has f = 0, and
+ * squares below 2^-149 vanish, which matters with eps = 0. gamma, residual and h are of type_io. */
 typedef enum { NM_ROWS_RMSNORM = 0, NM_ROWS_SWIGLU = 1 } nm_rows_op_t;
 typedef struct {
-  int64_t rows, cols;       /* of y; x has 2 * cols columns for NM_ROWS_SWIGLU */
+  int64_t rows, cols;       /* of y: rows < 2^24, cols <= 2^30; x has 2 * cols columns for NM_ROWS_SWIGLU */
   int32_t op;               /* nm_rows_op_t */
   int32_t type_io;          /* NM_F16 or NM_BF16 */
   int32_t type_x, type_y;   /* type_x: type_io or NM_I32; type_y: type_io or NM_I8 */
@@ -341,7 +344,9 @@ nm_status_t nm_swiglu(nm_rows_plan_t plan, const void* dX, const float* d_row_sc
  * for few tokens: up to 48 share one pass over the weights.
  * x is of type_y, or NM_I8 with one x_scale a token (1 where x is of type_y).
  * Up to 128 products of a group are summed in fp32 (exactly in int32 for NM_I8),
- * these sums times the scale in fp32, rounded once to type_y. */
+ * these sums times the scale in fp32, rounded once to type_y: where such a sum,
+ * its product with the scale or the sum of those passes fp32's range, y is
+ * infinite or NaN. */
 typedef struct {
   int64_t m, n, k;          /* m <= 2^24, n <= 2^20, k <= 2^20; sparse: k % 4 == 0 */
   int64_t group;            /* k per scale; 0: one scale a row. Otherwise a multiple of 32 (16-bit x) or 64

@@ -22,7 +22,7 @@ static nm_status_t w4_hip(hipError_t e) {
 static bool w4_aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 static const int64_t kW4MaxK = (int64_t)1 << 20;   // keeps offsets inside a row of x and of a row tile's codes in 32 bits
-static const int64_t kW4MaxM = (int64_t)1 << 24;   // the grid: m / 16 blocks of up to 1024 threads, under 2^32 threads
+static const int64_t kW4MaxM = (int64_t)1 << 24;   // the grid: m / 16 blocks of up to 512 threads, under 2^32 threads
 static const int64_t kW4MaxN = (int64_t)1 << 20;   // 48 columns a grid row, under 2^16 grid rows
 
 // One block a tile of 16 rows x 128 kept values, one thread a dword of eight
