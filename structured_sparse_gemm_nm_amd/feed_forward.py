@@ -33,7 +33,8 @@ _DTYPE_NAMES = {torch.float16: "f16", torch.bfloat16: "bf16"}
 
 # The 4-bit product passes over its weights once for every 48 tokens, the int8 2:4
 # product works on whole tiles of 128. One block of 4096 and 11008 features, in us:
-# 28 and 84 for one token, 50 and 123 for 48, 96 and 122 for 96, 144 and 75 for 128.
+# 30 and 84 for one token, 50 and 122 for 48, 74 and 122 for 49, 94 and 122 for 96,
+# 143 and 75 for 128.
 FEW_TOKENS = 96
 
 
@@ -149,16 +150,17 @@ class CompressedFeedForward:
 
     def _check(self, x, residual):
         """x is what a plan of the block can be made for, and no operand wants a gradient."""
-        if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (*x, residual)):
+        v, row, col = x
+        acc = v.dtype is torch.int32
+        if not acc and v.dtype is not self.dtype:
+            raise ValueError("x must be %s or int32 accumulators, got %s" % (self.dtype, v.dtype))
+        if (row is not None) != acc or (col is not None) != acc:
+            raise ValueError("row_scale and col_scale must be given exactly where x is int32")
+        if v.dim() != 2 or v.size(1) != self.hidden:
+            raise ValueError("x must be (tokens x %d), got %s" % (self.hidden, tuple(v.shape)))
+        if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (v, row, col, residual)):
             raise RuntimeError("the block has no backward pass: x and residual must not require a gradient "
                                "(detach them, or call it under torch.no_grad())")
-        if x.values.dim() != 2 or x.values.shape[1] != self.hidden:
-            raise ValueError("x must be (tokens x %d), got %s" % (self.hidden, tuple(x.values.shape)))
-        if x.values.dtype not in (self.dtype, torch.int32):
-            raise ValueError("x must be %s or int32 accumulators, got %s" % (self.dtype, x.values.dtype))
-        acc = x.values.dtype == torch.int32
-        if (x.row_scale is not None) != acc or (x.col_scale is not None) != acc:
-            raise ValueError("row_scale and col_scale must be given exactly where x is int32")
 
     def __call__(self, x, residual=None, few=None):
         """x: Rows or a 16-bit tensor (tokens x hidden); residual: 16-bit (tokens x hidden) or None.
