@@ -204,9 +204,9 @@ template <int OP, bool ACC> struct RowPiece {
 // with 256 threads and up to eight pieces, each waiting for its own loads, the norm
 // of 8192x4096 took 47 us, the activation 6.6 for 16x11008 and 94 for 4096x11008
 // accumulators. Memory bounds it: norm of 8192x4096 in 8 bits 41 us (235 MB, 5.7 TB/s),
-// of 4096x4096 accumulators 31 (168 MB, 5.4 TB/s), activation of 4096x11008
-// accumulators 82 (406 MB, 5.0 TB/s); few rows by latency: 16x11008 4.4 us, one row
-// of 4096 2.6.
+// of 4096x4096 accumulators 31.5 (168 MB, 5.3 TB/s), activation of 4096x11008
+// accumulators 82 (406 MB, 4.9 TB/s); few rows by latency: 16x11008 4.7 us, one row
+// of 4096 2.3.
 template <int OP, int IO, bool ACC, bool Y8, int C, bool TAIL>
 __global__ void __launch_bounds__(ROW_MOST) row_op_kernel(RowArgs A) {
   constexpr bool NORM = OP == NM_ROWS_RMSNORM;

@@ -227,10 +227,10 @@ __device__ __forceinline__ void w4_lds_order() {
 // matrix instruction's order has neighbouring lanes load from different tokens, a
 // cache line each; with XL they load a token's row along, and the wave turns the tile in
 // LDS. Scales come for 16 applications at a time: fetched with each tile, 8 bytes a lane,
-// they cost 32003x4096 (five tokens, two scales a tile) 15.6 us instead of 13.5 (70 MB,
+// they cost 32003x4096 (five tokens, two scales a tile) 15.6 us instead of 13.4 (70 MB,
 // 5.2 TB/s). 16384x4096, one f16 token, 8.2 us with R = 4 (34 MB, 4.2 TB/s; 10.3 with
-// R = 1), 16 tokens 8.9 (17.8); 32768x32768, four 8-bit tokens, 87 us (562 MB, 6.5 TB/s;
-// 97 with R = 1); 2:4 22016x4096, one bf16 token, 9.5 us (35 MB, 3.7 TB/s).
+// R = 1), 16 tokens 8.9 (17.8); 32768x32768, four 8-bit tokens, 88 us (562 MB, 6.4 TB/s;
+// 97 with R = 1); 2:4 22016x4096, one bf16 token, 9.2 us (35 MB, 3.8 TB/s).
 // Codes are loaded past the caches' reuse (nontemporal): x stays there.
 template <int XT, bool YB, bool SPARSE, bool ZEROS, int F, int NT, int R, bool XL>
 __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
