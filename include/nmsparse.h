@@ -382,6 +382,67 @@ nm_status_t nm_w4_pack(nm_w4_plan_t plan, const void* d_codes, const void* d_sca
 nm_status_t nm_w4_matvec(nm_w4_plan_t plan, const void* d_packed, const void* dX, const float* d_x_scale, void* dY,
                          void* stream);
 
+/* ------------------------------------------------------------------------
+ * What the products hand on: the operators below take a product's 16-bit rows,
+ * or the int32 accumulators of an int8 product, whose value is x * row_scale[row]
+ * * col_scale[column]. Plans, ownership, streams and errors as above; vectors with
+ * one entry a row (row scales, positions, tokens, gradients of a row's value) need
+ * the alignment of their elements only.
+ * ------------------------------------------------------------------------ */
+
+/* Norms of queries and keys for each head, with the rotation by position in the
+ * same pass. A row (token) of x holds heads_q query heads, then heads_k key heads,
+ * then heads_v value heads of head_dim elements each; y has the same columns.
+ *  query and key heads: v = gamma * u / sqrt(mean(u^2) + eps) over the head, then
+ *    each pair (a, b) of the first rotary_dim elements becomes
+ *    (a * c - b * s, b * c + a * s), with c = table[position][i] and
+ *    s = table[position][rotary_dim / 2 + i] for the i-th pair: elements i and
+ *    i + rotary_dim / 2 (NM_PAIRS_HALVES), or 2i and 2i + 1 (NM_PAIRS_NEIGHBOURS);
+ *  value heads: y = u.
+ * Everything is computed in fp32 and rounded once to type_io; a head's sum of
+ * squares has fp32's range, as a row's has in nm_rmsnorm, and a head of zeros with
+ * eps = 0 is NaN. A row whose position is negative holds no token: its y stays as it
+ * was. A position of table_rows or more has no angles: the turned elements are NaN. */
+typedef enum { NM_PAIRS_HALVES = 0, NM_PAIRS_NEIGHBOURS = 1 } nm_pairs_t;
+typedef struct {
+  int64_t rows;             /* tokens, < 2^24 */
+  int32_t heads_q, heads_k, heads_v; /* heads_q >= 1, the others >= 0; at most 65536 each */
+  int32_t head_dim;         /* a multiple of 8, up to 512 */
+  int32_t rotary_dim;       /* a multiple of 8, up to head_dim; 0: no rotation */
+  int32_t pairs;            /* nm_pairs_t */
+  int32_t type_io;          /* y and the gains: NM_F16 or NM_BF16 */
+  int32_t type_x;           /* type_io or NM_I32 */
+  int64_t table_rows;       /* positions that the table holds, up to 2^31 */
+  int64_t ldx, ldy;         /* rows of x (and its gradient), of y (and its gradient) */
+  float eps;                /* finite and >= 0 */
+} nm_heads_problem_t;
+typedef struct nm_heads_plan* nm_heads_plan_t;
+nm_status_t nm_heads_plan_init(nm_heads_plan_t* plan, const nm_heads_problem_t* problem);
+nm_status_t nm_heads_plan_destroy(nm_heads_plan_t plan);
+
+/* d_gamma_q, d_gamma_k: head_dim elements of type_io (d_gamma_k is read where there
+ * are key heads); d_positions: rows; d_table: table_rows x rotary_dim floats (not read
+ * where rotary_dim is 0). d_row_scale (rows) and d_col_scale (columns) are given exactly
+ * where x is NM_I32. dY may equal dX where x is of type_io and ldx == ldy. */
+nm_status_t nm_head_norm_rope(nm_heads_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                              const void* d_gamma_q, const void* d_gamma_k, const int64_t* d_positions,
+                              const float* d_table, void* dY, void* stream);
+
+/* The gradient, for x of type_io (NM_ERR_UNSUPPORTED for accumulators): from x, the
+ * forward's other inputs and d_grad_y (rows x columns of type_io, ldy), d_grad_x (of
+ * type_io, ldx; it may equal d_grad_y where ldx == ldy) and, where wanted, the gains'
+ * gradients summed over tokens and heads (head_dim elements of type_io each;
+ * d_grad_gamma_k exactly with d_grad_gamma_q where there are key heads). A row that
+ * holds no token has gradient zero. The sums are taken in fp32, those of the blocks
+ * in 64 bits, in an order that the plan alone decides, and rounded once. d_workspace:
+ * nm_heads_workspace_size bytes where the gains' gradients are wanted; scratch, as
+ * for nm_spmm. */
+nm_status_t nm_heads_workspace_size(nm_heads_plan_t plan, size_t* bytes);
+nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, const void* d_gamma_q, const void* d_gamma_k,
+                                       const int64_t* d_positions, const float* d_table, const void* d_grad_y,
+                                       void* d_grad_x, void* d_grad_gamma_q, void* d_grad_gamma_k, void* d_workspace,
+                                       void* stream);
+
 /* Name of the SpMM kernel the plan dispatches to (static string). */
 const char* nm_plan_kernel_name(nm_plan_t plan);
 

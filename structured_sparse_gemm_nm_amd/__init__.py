@@ -56,6 +56,13 @@ class nm_w4_problem_t(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
+class nm_heads_problem_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("heads_v", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("type_io", ctypes.c_int32), ("type_x", ctypes.c_int32),
+                ("table_rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
 _lib = _calls = _calls_error = None
 
 
@@ -112,6 +119,12 @@ def lib():
         L.nm_w4_sizes.argtypes = [P, ctypes.POINTER(S), ctypes.POINTER(I64), ctypes.POINTER(I64), ctypes.POINTER(I64)]
         L.nm_w4_pack.restype = st; L.nm_w4_pack.argtypes = [P] * 7
         L.nm_w4_matvec.restype = st; L.nm_w4_matvec.argtypes = [P] * 6
+        L.nm_heads_plan_init.restype = st
+        L.nm_heads_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_heads_problem_t)]
+        L.nm_heads_plan_destroy.restype = st; L.nm_heads_plan_destroy.argtypes = [P]
+        L.nm_heads_workspace_size.restype = st; L.nm_heads_workspace_size.argtypes = [P, ctypes.POINTER(S)]
+        L.nm_head_norm_rope.restype = st; L.nm_head_norm_rope.argtypes = [P] * 10
+        L.nm_head_norm_rope_backward.restype = st; L.nm_head_norm_rope_backward.argtypes = [P] * 12
         L.nm_status_string.restype = ctypes.c_char_p; L.nm_status_string.argtypes = [st]
         L.nm_last_error.restype = ctypes.c_char_p; L.nm_last_error.argtypes = []
         L.nm_version.restype = I32; L.nm_version.argtypes = []
@@ -379,7 +392,7 @@ class _LayerPlan:
     """Owns a plan handle of the operators around the product."""
 
     _destroy = None
-    _norm_call = _gate_call = _product_call = None
+    _norm_call = _gate_call = _product_call = _back_call = None
 
     def __init__(self, handle, problem):
         self.handle = handle.value
@@ -396,7 +409,7 @@ class _LayerPlan:
         return calls.Call(ctypes.cast(fn, ctypes.c_void_p).value, self.handle, main, specs)
 
     def destroy(self):
-        self._norm_call = self._gate_call = self._product_call = None
+        self._norm_call = self._gate_call = self._product_call = self._back_call = None
         if self.handle is not None:
             getattr(lib(), self._destroy)(self.handle)
             self.handle = None
@@ -553,6 +566,91 @@ def nm_w4_matvec(plan, d_packed, dX, dY, x_scale=None, stream=None):
         _address(dX, "x", plan.x_dtype, plan._x, ldx, dev),
         _address(x_scale, "x_scale", torch.float32, plan._x[:1], None, dev),
         _address(dY, "y", plan.y_dtype, plan._y, ldy, dev), stream))
+
+
+# ---- what the products hand on: head norms with rotation ----
+
+NM_PAIRS_HALVES, NM_PAIRS_NEIGHBOURS = 0, 1
+PAIRS = {"halves": NM_PAIRS_HALVES, "neighbours": NM_PAIRS_NEIGHBOURS}
+
+
+def _workspace_size(name, handle):
+    n = ctypes.c_size_t()
+    _check(getattr(lib(), name)(handle, ctypes.byref(n)))
+    return n.value
+
+
+class HeadsPlan(_LayerPlan):
+    """Plan of nm_head_norm_rope and its gradient."""
+
+    _destroy = "nm_heads_plan_destroy"
+
+    def __init__(self, handle, problem, io, x):
+        super().__init__(handle, problem)
+        p = problem
+        self.rows, self.cols = p.rows, (p.heads_q + p.heads_k + p.heads_v) * p.head_dim
+        self.io_dtype, self.x_dtype = TORCH_DTYPES[io], TORCH_DTYPES[x]
+        self.workspace_bytes = _workspace_size("nm_heads_workspace_size", self.handle)
+        f32, shape, dim = torch.float32, (p.rows, self.cols), (p.head_dim,)
+        gain, x_spec, y_spec = (self.io_dtype, dim, None), (self.x_dtype, shape, p.ldx), (self.io_dtype, shape, p.ldy)
+        # a table of no columns has no address to give
+        table = (f32, (p.table_rows, p.rotary_dim), max(1, p.rotary_dim))
+        common = gain, gain, (torch.int64, (p.rows,), None), table
+        self._specs = (x_spec, (f32, shape[:1], None), (f32, shape[1:], None)) + common + (y_spec,)
+        self._back_specs = (x_spec,) + common + (y_spec, (self.io_dtype, shape, p.ldx), gain, gain,
+                                                 (torch.uint8, (self.workspace_bytes,), None))
+        self._norm_call = self._call("nm_head_norm_rope", 0, *self._specs)
+        if x != "i32":
+            self._back_call = self._call("nm_head_norm_rope_backward", 0, *self._back_specs)
+
+    def empty_workspace(self, device="cuda"):
+        """Workspace of the gains' gradients."""
+        return torch.empty((self.workspace_bytes,), dtype=torch.uint8, device=device)
+
+
+def nm_heads_plan_init(rows, heads_q, heads_k, heads_v, head_dim, rotary_dim, pairs="halves", table_rows=0, dtype="f16",
+                       x_dtype=None, ldx=None, ldy=None, eps=1e-6):
+    """Plan of the norms of query and key heads with their rotation (host only). pairs: "halves" (i, i + rotary_dim / 2)
+    or "neighbours" (2i, 2i + 1); table_rows: the positions that the table of angles holds; dtype: the 16-bit type of y
+    and the gains; x_dtype: dtype, or "i32" for an int8 product's accumulators."""
+    if pairs not in PAIRS:
+        raise ValueError("pairs must be one of %s, got %r" % (sorted(PAIRS), pairs))
+    x_dtype = x_dtype or dtype
+    p = nm_heads_problem_t()
+    p.rows, p.heads_q, p.heads_k, p.heads_v, p.head_dim, p.rotary_dim = rows, heads_q, heads_k, heads_v, head_dim, rotary_dim
+    p.pairs, p.table_rows, p.eps = PAIRS[pairs], table_rows, eps
+    p.type_io, p.type_x = _dtype_code(dtype), _dtype_code(x_dtype)
+    cols = max(1, (heads_q + heads_k + heads_v) * head_dim)
+    p.ldx = ldx if ldx is not None else cols
+    p.ldy = ldy if ldy is not None else cols
+    h = ctypes.c_void_p()
+    _check(lib().nm_heads_plan_init(ctypes.byref(h), ctypes.byref(p)))
+    return HeadsPlan(h, p, dtype, x_dtype)
+
+
+def _layer_call(plan, call, entry, specs, names, operands, main, stream):
+    """One call of a layer operator: through the call extension, or with its operands checked here."""
+    status = call(*operands, stream) if call else -1
+    if status < 0:
+        dev, stream = _where(operands[main], stream)
+        status = getattr(lib(), entry)(plan.handle, *(_address(t, n, *s, dev) for t, n, s in zip(operands, names, specs)),
+                                       stream)
+    _check(status)
+
+
+def nm_head_norm_rope(plan, dX, gamma_q, gamma_k, positions, table, dY, row_scale=None, col_scale=None, stream=None):
+    """Query and key heads normed and turned by their row's position, value heads as they are."""
+    _layer_call(plan, plan._norm_call, "nm_head_norm_rope", plan._specs,
+                ("x", "row_scale", "col_scale", "gamma_q", "gamma_k", "positions", "table", "y"),
+                (dX, row_scale, col_scale, gamma_q, gamma_k, positions, table, dY), 0, stream)
+
+
+def nm_head_norm_rope_backward(plan, dX, gamma_q, gamma_k, positions, table, grad_y, grad_x, dgamma_q=None, dgamma_k=None,
+                               workspace=None, stream=None):
+    """Gradients of x and, where they are given, of both gains (workspace: plan.empty_workspace())."""
+    _layer_call(plan, plan._back_call, "nm_head_norm_rope_backward", plan._back_specs,
+                ("x", "gamma_q", "gamma_k", "positions", "table", "grad_y", "grad_x", "dgamma_q", "dgamma_k", "workspace"),
+                (dX, gamma_q, gamma_k, positions, table, grad_y, grad_x, dgamma_q, dgamma_k, workspace), 0, stream)
 
 
 NM_ALG_AUTO, NM_ALG_TILE128, NM_ALG_TILE256X128, NM_ALG_TILE256, NM_ALG_COUNT = range(5)

@@ -20,7 +20,7 @@
 
 namespace {
 
-constexpr int kMost = 8;   // operands of an entry point
+constexpr int kMost = 11;  // operands of an entry point
 
 struct Spec {
   c10::ScalarType type;
@@ -70,9 +70,17 @@ int32_t enter(void* fn, void* h, void* const* a, int n, void* s) {
   switch (n) {
     case 4: return reinterpret_cast<int32_t (*)(P, P, P, P, P, P)>(fn)(h, a[0], a[1], a[2], a[3], s);
     case 5: return reinterpret_cast<int32_t (*)(P, P, P, P, P, P, P)>(fn)(h, a[0], a[1], a[2], a[3], a[4], s);
-    default:
+    case 7:
+      return reinterpret_cast<int32_t (*)(P, P, P, P, P, P, P, P, P)>(fn)(h, a[0], a[1], a[2], a[3], a[4], a[5], a[6], s);
+    case 8:
       return reinterpret_cast<int32_t (*)(P, P, P, P, P, P, P, P, P, P)>(fn)(h, a[0], a[1], a[2], a[3], a[4], a[5],
                                                                              a[6], a[7], s);
+    case 10:
+      return reinterpret_cast<int32_t (*)(P, P, P, P, P, P, P, P, P, P, P, P)>(fn)(
+          h, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], s);
+    default:
+      return reinterpret_cast<int32_t (*)(P, P, P, P, P, P, P, P, P, P, P, P, P)>(fn)(
+          h, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], s);
   }
 }
 
@@ -120,8 +128,8 @@ int init(PyObject* self, PyObject* args, PyObject*) {
   c->plan = PyLong_AsVoidPtr(plan);
   if (PyErr_Occurred()) return -1;
   const Py_ssize_t n = PyTuple_GET_SIZE(specs);
-  if ((n != 4 && n != 5 && n != 8) || c->main < 0 || c->main >= n || !c->fn || !c->plan) {
-    PyErr_SetString(PyExc_ValueError, "an entry point with 4, 5 or 8 operands and a plan is expected");
+  if ((n != 4 && n != 5 && n != 7 && n != 8 && n != 10 && n != 11) || c->main < 0 || c->main >= n || !c->fn || !c->plan) {
+    PyErr_SetString(PyExc_ValueError, "an entry point with 4, 5, 7, 8, 10 or 11 operands and a plan is expected");
     return -1;
   }
   for (Py_ssize_t i = 0; i < n; i++) {
