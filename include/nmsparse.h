@@ -102,7 +102,7 @@ typedef enum {
   NM_ERR_HIP = 5          /* a HIP runtime call or kernel launch failed */
 } nm_status_t;
 
-typedef enum { NM_F16 = 0, NM_BF16 = 1, NM_I8 = 2, NM_I32 = 3 } nm_dtype_t;
+typedef enum { NM_F16 = 0, NM_BF16 = 1, NM_I8 = 2, NM_I32 = 3, NM_F32 = 4 /* logits only */ } nm_dtype_t;
 typedef enum { NM_OP_N = 0, NM_OP_T = 1 } nm_op_t;
 /* Storage order of C and D. NM_ROW_MAJOR: element (i, j) at i * ld + j
  * (ld >= n). NM_COL_MAJOR: element (i, j) at j * ld + i (ld >= m), the
@@ -442,6 +442,51 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
                                        const int64_t* d_positions, const float* d_table, const void* d_grad_y,
                                        void* d_grad_x, void* d_grad_gamma_q, void* d_grad_gamma_k, void* d_workspace,
                                        void* stream);
+
+/* Log probabilities of given tokens, entropy and the most probable alternatives,
+ * from rows of logits x: z = scale * x, p = exp(z) / sum(exp(z)),
+ *   logprob[row] = log p of d_tokens[row], entropy[row] = -sum(p log p),
+ * and the top largest logits' columns and log probabilities in their order, the
+ * lower of two equal ones' columns first. A logit is the fp32 value of x (of
+ * NM_I32: (x * row_scale) * col_scale, each product rounded to fp32); sums are
+ * taken in fp32, against the row's largest logit.
+ *  - A negative token is none: its log probability is 0. A token of cols or more: NaN.
+ *  - Logits of -infinity have probability 0 and no part in the entropy. A row of
+ *    nothing else: log probabilities -infinity, entropy 0.
+ *  - A row that holds a NaN or +infinity has no distribution: its values are NaN, its
+ *    alternatives NaN with column -1. */
+typedef struct {
+  int64_t rows, cols;       /* rows < 2^24, cols 1 to 2^22 */
+  int32_t type_x;           /* NM_F16, NM_BF16, NM_F32 or NM_I32 */
+  int32_t top;              /* alternatives a row: 0 to 32, at most cols */
+  int64_t ldx, ldg;         /* rows of x, and of its gradient (not read for NM_I32) */
+  float scale;              /* one over the temperature: finite and > 0 */
+} nm_logprobs_problem_t;
+typedef struct nm_logprobs_plan* nm_logprobs_plan_t;
+nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_problem_t* problem);
+nm_status_t nm_logprobs_plan_destroy(nm_logprobs_plan_t plan);
+nm_status_t nm_logprobs_workspace_size(nm_logprobs_plan_t plan, size_t* bytes);
+
+/* d_tokens and d_logprob (rows each) are given together or not at all; d_entropy
+ * (rows) and d_stats (rows x 2 floats, for the gradient only) may be NULL;
+ * d_top_logprob and d_top_index (rows x top) are given exactly where top > 0.
+ * d_row_scale (rows) and d_col_scale (cols) exactly where x is NM_I32. d_workspace:
+ * nm_logprobs_workspace_size bytes (few long rows are cut into slices); scratch, as
+ * for nm_spmm, NULL where the size is 0. */
+nm_status_t nm_logprobs(nm_logprobs_plan_t plan, const void* dX, const float* d_row_scale, const float* d_col_scale,
+                        const int64_t* d_tokens, float* d_logprob, float* d_entropy, float* d_stats, float* d_top_logprob,
+                        int64_t* d_top_index, void* d_workspace, void* stream);
+
+/* The logits' gradient, in x's type (NM_ERR_UNSUPPORTED for NM_I32): with g and h the
+ * gradients of a row's log probability and of its entropy H,
+ *   dx_i = scale * (g * ([i == token] - p_i) - h * p_i * (log p_i + H)).
+ * One of d_grad_logprob (with d_tokens) and d_grad_entropy (with d_entropy, the
+ * forward's) may be NULL: that term is left out. A row whose token is none has no g, a
+ * row of -infinity alone gradient 0. d_stats comes from nm_logprobs on the same x and
+ * scale. d_grad_x may equal dX where ldg == ldx. */
+nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const int64_t* d_tokens, const float* d_stats,
+                                 const float* d_entropy, const float* d_grad_logprob, const float* d_grad_entropy,
+                                 void* d_grad_x, void* stream);
 
 /* Name of the SpMM kernel the plan dispatches to (static string). */
 const char* nm_plan_kernel_name(nm_plan_t plan);

@@ -18,12 +18,12 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnmsparse.so")
 
 NM_OK, NM_ERR_INVALID_ARG, NM_ERR_SHAPE, NM_ERR_ALIGN, NM_ERR_UNSUPPORTED, NM_ERR_HIP = range(6)
-NM_F16, NM_BF16, NM_I8, NM_I32 = range(4)
+NM_F16, NM_BF16, NM_I8, NM_I32, NM_F32 = range(5)
 NM_OP_N, NM_OP_T = 0, 1
 NM_PRUNE_1D, NM_PRUNE_TILE4X4 = 0, 1
 
 DTYPES = {"f16": (NM_F16, NM_F16), "bf16": (NM_BF16, NM_BF16), "i8": (NM_I8, NM_I32)}
-TORCH_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "i8": torch.int8, "i32": torch.int32}
+TORCH_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "i8": torch.int8, "i32": torch.int32, "f32": torch.float32}
 MODES = {"1d": NM_PRUNE_1D, "tile": NM_PRUNE_TILE4X4}
 
 
@@ -61,6 +61,11 @@ class nm_heads_problem_t(ctypes.Structure):
                 ("heads_v", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
                 ("pairs", ctypes.c_int32), ("type_io", ctypes.c_int32), ("type_x", ctypes.c_int32),
                 ("table_rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
+class nm_logprobs_problem_t(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("type_x", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldg", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
 _lib = _calls = _calls_error = None
@@ -125,6 +130,12 @@ def lib():
         L.nm_heads_workspace_size.restype = st; L.nm_heads_workspace_size.argtypes = [P, ctypes.POINTER(S)]
         L.nm_head_norm_rope.restype = st; L.nm_head_norm_rope.argtypes = [P] * 10
         L.nm_head_norm_rope_backward.restype = st; L.nm_head_norm_rope_backward.argtypes = [P] * 12
+        L.nm_logprobs_plan_init.restype = st
+        L.nm_logprobs_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_logprobs_problem_t)]
+        L.nm_logprobs_plan_destroy.restype = st; L.nm_logprobs_plan_destroy.argtypes = [P]
+        L.nm_logprobs_workspace_size.restype = st; L.nm_logprobs_workspace_size.argtypes = [P, ctypes.POINTER(S)]
+        L.nm_logprobs.restype = st; L.nm_logprobs.argtypes = [P] * 12
+        L.nm_logprobs_backward.restype = st; L.nm_logprobs_backward.argtypes = [P] * 9
         L.nm_status_string.restype = ctypes.c_char_p; L.nm_status_string.argtypes = [st]
         L.nm_last_error.restype = ctypes.c_char_p; L.nm_last_error.argtypes = []
         L.nm_version.restype = I32; L.nm_version.argtypes = []
@@ -568,7 +579,7 @@ def nm_w4_matvec(plan, d_packed, dX, dY, x_scale=None, stream=None):
         _address(dY, "y", plan.y_dtype, plan._y, ldy, dev), stream))
 
 
-# ---- what the products hand on: head norms with rotation ----
+# ---- what the products hand on: head norms with rotation, log probabilities ----
 
 NM_PAIRS_HALVES, NM_PAIRS_NEIGHBOURS = 0, 1
 PAIRS = {"halves": NM_PAIRS_HALVES, "neighbours": NM_PAIRS_NEIGHBOURS}
@@ -651,6 +662,66 @@ def nm_head_norm_rope_backward(plan, dX, gamma_q, gamma_k, positions, table, gra
     _layer_call(plan, plan._back_call, "nm_head_norm_rope_backward", plan._back_specs,
                 ("x", "gamma_q", "gamma_k", "positions", "table", "grad_y", "grad_x", "dgamma_q", "dgamma_k", "workspace"),
                 (dX, gamma_q, gamma_k, positions, table, grad_y, grad_x, dgamma_q, dgamma_k, workspace), 0, stream)
+
+
+_LOGITS = {"f16": NM_F16, "bf16": NM_BF16, "f32": NM_F32, "i32": NM_I32}
+
+
+class LogprobsPlan(_LayerPlan):
+    """Plan of nm_logprobs and its gradient."""
+
+    _destroy = "nm_logprobs_plan_destroy"
+
+    def __init__(self, handle, problem, x):
+        super().__init__(handle, problem)
+        p = problem
+        self.rows, self.cols, self.top, self.x_dtype = p.rows, p.cols, p.top, TORCH_DTYPES[x]
+        self.workspace_bytes = _workspace_size("nm_logprobs_workspace_size", self.handle)
+        f32, i64 = torch.float32, torch.int64
+        x_spec, row, top = (self.x_dtype, (p.rows, p.cols), p.ldx), (f32, (p.rows,), None), (p.rows, p.top)
+        tokens, stats = (i64, (p.rows,), None), (f32, (p.rows, 2), 2)
+        self._specs = (x_spec, row, (f32, (p.cols,), None), tokens, row, row, stats, (f32, top, max(1, p.top)),
+                       (i64, top, max(1, p.top)), (torch.uint8, (self.workspace_bytes,), None))
+        self._back_specs = x_spec, tokens, stats, row, row, row, (self.x_dtype, (p.rows, p.cols), max(1, p.ldg))
+        self._norm_call = self._call("nm_logprobs", 0, *self._specs)
+        if x != "i32":
+            self._back_call = self._call("nm_logprobs_backward", 0, *self._back_specs)
+
+    def empty_workspace(self, device="cuda"):
+        """Workspace of nm_logprobs (None where it needs none)."""
+        n = self.workspace_bytes
+        return torch.empty((n,), dtype=torch.uint8, device=device) if n else None
+
+
+def nm_logprobs_plan_init(rows, cols, dtype="f16", top=0, scale=1.0, ldx=None, ldg=None):
+    """Plan of the log probabilities of rows of logits (host only). dtype: "f16", "bf16", "f32", or "i32" for an int8
+    product's accumulators; top: alternatives a row; scale: one over the temperature; ldg: rows of the gradient (ldx
+    unless given)."""
+    if dtype not in _LOGITS:
+        raise ValueError("dtype must be one of %s, got %r" % (sorted(_LOGITS), dtype))
+    p = nm_logprobs_problem_t()
+    p.rows, p.cols, p.type_x, p.top, p.scale = rows, cols, _LOGITS[dtype], top, scale
+    p.ldx = ldx if ldx is not None else max(1, cols)
+    p.ldg = ldg if ldg is not None else p.ldx
+    h = ctypes.c_void_p()
+    _check(lib().nm_logprobs_plan_init(ctypes.byref(h), ctypes.byref(p)))
+    return LogprobsPlan(h, p, dtype)
+
+
+def nm_logprobs(plan, dX, tokens=None, logprob=None, entropy=None, stats=None, top_logprob=None, top_index=None,
+                row_scale=None, col_scale=None, workspace=None, stream=None):
+    """Log probabilities of the rows' tokens, their entropy, and the plan's number of alternatives; stats (rows x 2
+    floats) is what the gradient reads."""
+    _layer_call(plan, plan._norm_call, "nm_logprobs", plan._specs,
+                ("x", "row_scale", "col_scale", "tokens", "logprob", "entropy", "stats", "top_logprob", "top_index", "workspace"),
+                (dX, row_scale, col_scale, tokens, logprob, entropy, stats, top_logprob, top_index, workspace), 0, stream)
+
+
+def nm_logprobs_backward(plan, dX, tokens, stats, grad_x, g_logprob=None, g_entropy=None, entropy=None, stream=None):
+    """The logits' gradient from those of the log probabilities and of the entropy."""
+    _layer_call(plan, plan._back_call, "nm_logprobs_backward", plan._back_specs,
+                ("x", "tokens", "stats", "entropy", "g_logprob", "g_entropy", "grad_x"),
+                (dX, tokens, stats, entropy, g_logprob, g_entropy, grad_x), 0, stream)
 
 
 NM_ALG_AUTO, NM_ALG_TILE128, NM_ALG_TILE256X128, NM_ALG_TILE256, NM_ALG_COUNT = range(5)

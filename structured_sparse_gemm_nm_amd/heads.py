@@ -26,9 +26,12 @@ def rotation_table(positions, rotary_dim, base=10000.0, device="cuda"):
 
 
 def _rows_on_16_bytes(t):
-    """t, or a copy of it whose rows the library takes."""
-    ok = t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) * t.element_size() % 16 == 0
-    return t if ok and t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+    """t, or a copy of it in rows that the library takes: on 16-byte boundaries."""
+    step = 16 // t.element_size()
+    if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % step == 0 and t.data_ptr() % 16 == 0:
+        return t
+    out = torch.empty((t.shape[0], (t.shape[1] + step - 1) // step * step), dtype=t.dtype, device=t.device)[:, :t.shape[1]]
+    return out.copy_(t)
 
 
 def _plan(x, heads, dim, table, gamma, pairs, eps):
