@@ -488,6 +488,42 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
                                  const float* d_entropy, const float* d_grad_logprob, const float* d_grad_entropy,
                                  void* d_grad_x, void* stream);
 
+/* Low-rank adapters of many requests beside a shared projection:
+ *   y[j] = base[j] + d_scale[a] * x_scale[j] * B[a] (A[a] x[j]),  a = d_index[j]
+ * for n tokens x (n x k; x_scale is 1 where x is of type_y). A holds the adapters one
+ * after the other, rank rows of k each (adapters * rank rows, lda), B m rows of rank
+ * each (adapters * m rows, rank elements apart); smaller ranks are padded with zeros.
+ * base (n x m, ldc) is what the projection gave: of type_y, where it may be y itself,
+ * or nm_spmm's int32 accumulators, whose value is base * row_scale * col_scale.
+ *  - A negative index names no adapter: y[j] = base[j] (a row that is its own base is
+ *    not written). An index of `adapters` or more: the row is NaN.
+ *  - A x is summed in fp32 and meets B as two 16-bit parts: the first rounded to type_y
+ *    (f16: after the token's largest was brought to 1 by a power of two), the second
+ *    what that left over, so that it keeps 2^-16 (bf16) or 2^-22 (f16, of the token's
+ *    largest) of its value. The rest is fp32, rounded once to type_y.
+ *  - A token's row depends on nothing but that token, its adapter and n.
+ * There is no backward pass: adapters that are served are constants. */
+typedef struct {
+  int64_t m, n, k;          /* m <= 2^24, n <= 2^20, 1 <= k <= 2^20 */
+  int32_t adapters;         /* 1 to 2^20 */
+  int32_t rank;             /* a multiple of 8, 8 to 128 */
+  int32_t type_y;           /* y, A and B: NM_F16 or NM_BF16 */
+  int32_t type_x;           /* type_y or NM_I8 */
+  int32_t type_base;        /* type_y or NM_I32 */
+  int64_t ldx, lda, ldc, ldy;
+} nm_lora_problem_t;
+typedef struct nm_lora_plan* nm_lora_plan_t;
+nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* problem);
+nm_status_t nm_lora_plan_destroy(nm_lora_plan_t plan);
+nm_status_t nm_lora_workspace_size(nm_lora_plan_t plan, size_t* bytes);
+
+/* d_x_scale (n floats) is given exactly where x is NM_I8, d_row_scale (n) and
+ * d_col_scale (m) exactly where base is NM_I32. d_scale: adapters floats. d_workspace:
+ * nm_lora_workspace_size bytes; scratch, as for nm_spmm. */
+nm_status_t nm_lora(nm_lora_plan_t plan, const void* dX, const float* d_x_scale, const void* dA, const void* dB,
+                    const float* d_scale, const int64_t* d_index, const void* d_base, const float* d_row_scale,
+                    const float* d_col_scale, void* dY, void* d_workspace, void* stream);
+
 /* Name of the SpMM kernel the plan dispatches to (static string). */
 const char* nm_plan_kernel_name(nm_plan_t plan);
 

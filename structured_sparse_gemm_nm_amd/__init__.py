@@ -68,6 +68,13 @@ class nm_logprobs_problem_t(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldg", ctypes.c_int64), ("scale", ctypes.c_float)]
 
 
+class nm_lora_problem_t(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("adapters", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("type_y", ctypes.c_int32), ("type_x", ctypes.c_int32),
+                ("type_base", ctypes.c_int32), ("ldx", ctypes.c_int64), ("lda", ctypes.c_int64), ("ldc", ctypes.c_int64),
+                ("ldy", ctypes.c_int64)]
+
+
 _lib = _calls = _calls_error = None
 
 
@@ -136,6 +143,11 @@ def lib():
         L.nm_logprobs_workspace_size.restype = st; L.nm_logprobs_workspace_size.argtypes = [P, ctypes.POINTER(S)]
         L.nm_logprobs.restype = st; L.nm_logprobs.argtypes = [P] * 12
         L.nm_logprobs_backward.restype = st; L.nm_logprobs_backward.argtypes = [P] * 9
+        L.nm_lora_plan_init.restype = st
+        L.nm_lora_plan_init.argtypes = [ctypes.POINTER(P), ctypes.POINTER(nm_lora_problem_t)]
+        L.nm_lora_plan_destroy.restype = st; L.nm_lora_plan_destroy.argtypes = [P]
+        L.nm_lora_workspace_size.restype = st; L.nm_lora_workspace_size.argtypes = [P, ctypes.POINTER(S)]
+        L.nm_lora.restype = st; L.nm_lora.argtypes = [P] * 13
         L.nm_status_string.restype = ctypes.c_char_p; L.nm_status_string.argtypes = [st]
         L.nm_last_error.restype = ctypes.c_char_p; L.nm_last_error.argtypes = []
         L.nm_version.restype = I32; L.nm_version.argtypes = []
@@ -579,7 +591,7 @@ def nm_w4_matvec(plan, d_packed, dX, dY, x_scale=None, stream=None):
         _address(dY, "y", plan.y_dtype, plan._y, ldy, dev), stream))
 
 
-# ---- what the products hand on: head norms with rotation, log probabilities ----
+# ---- what the products hand on: head norms with rotation, log probabilities, adapters ----
 
 NM_PAIRS_HALVES, NM_PAIRS_NEIGHBOURS = 0, 1
 PAIRS = {"halves": NM_PAIRS_HALVES, "neighbours": NM_PAIRS_NEIGHBOURS}
@@ -722,6 +734,55 @@ def nm_logprobs_backward(plan, dX, tokens, stats, grad_x, g_logprob=None, g_entr
     _layer_call(plan, plan._back_call, "nm_logprobs_backward", plan._back_specs,
                 ("x", "tokens", "stats", "entropy", "g_logprob", "g_entropy", "grad_x"),
                 (dX, tokens, stats, entropy, g_logprob, g_entropy, grad_x), 0, stream)
+
+
+class LoraPlan(_LayerPlan):
+    """Plan of nm_lora."""
+
+    _destroy = "nm_lora_plan_destroy"
+
+    def __init__(self, handle, problem, y, x, base):
+        super().__init__(handle, problem)
+        p = problem
+        self.m, self.n, self.k, self.rank, self.adapters = p.m, p.n, p.k, p.rank, p.adapters
+        self.y_dtype, self.x_dtype, self.base_dtype = TORCH_DTYPES[y], TORCH_DTYPES[x], TORCH_DTYPES[base]
+        self.workspace_bytes = _workspace_size("nm_lora_workspace_size", self.handle)
+        f32, dt, out, row = torch.float32, self.y_dtype, (p.n, p.m), (torch.float32, (p.n,), None)
+        self._specs = ((self.x_dtype, (p.n, p.k), p.ldx), row, (dt, (p.adapters * p.rank, p.k), p.lda),
+                       (dt, (p.adapters * p.m, p.rank), p.rank), (f32, (p.adapters,), None), (torch.int64, (p.n,), None),
+                       (self.base_dtype, out, p.ldc), row, (f32, (p.m,), None), (dt, out, p.ldy),
+                       (torch.uint8, (self.workspace_bytes,), None))
+        self._product_call = self._call("nm_lora", 0, *self._specs)
+
+    def empty_workspace(self, device="cuda"):
+        return torch.empty((self.workspace_bytes,), dtype=torch.uint8, device=device)
+
+
+def nm_lora_plan_init(m, n, k, rank, adapters, dtype="f16", x_dtype=None, base_dtype=None, ldx=None, lda=None, ldc=None,
+                      ldy=None):
+    """Plan of n tokens' low-rank adapters beside a projection of k to m features (host only). dtype: the 16-bit type of
+    y, A and B; x_dtype: dtype, or "i8" with one scale a token; base_dtype: dtype, or "i32" for an int8 product's
+    accumulators."""
+    x_dtype, base_dtype = x_dtype or dtype, base_dtype or dtype
+    p = nm_lora_problem_t()
+    p.m, p.n, p.k, p.rank, p.adapters = m, n, k, rank, adapters
+    p.type_y, p.type_x, p.type_base = _dtype_code(dtype), _dtype_code(x_dtype), _dtype_code(base_dtype)
+    p.ldx = ldx if ldx is not None else max(1, k)
+    p.lda = lda if lda is not None else max(1, k)
+    p.ldc = ldc if ldc is not None else max(1, m)
+    p.ldy = ldy if ldy is not None else max(1, m)
+    h = ctypes.c_void_p()
+    _check(lib().nm_lora_plan_init(ctypes.byref(h), ctypes.byref(p)))
+    return LoraPlan(h, p, dtype, x_dtype, base_dtype)
+
+
+def nm_lora(plan, dX, dA, dB, scale, index, base, dY, x_scale=None, row_scale=None, col_scale=None, workspace=None,
+            stream=None):
+    """y = base + scale[a] B[a] (A[a] x) by rows, a the adapter that index names (negative: none). dA: the adapters' rank
+    rows of k, one adapter after the other; dB: their m rows of rank."""
+    _layer_call(plan, plan._product_call, "nm_lora", plan._specs,
+                ("x", "x_scale", "A", "B", "scale", "index", "base", "row_scale", "col_scale", "y", "workspace"),
+                (dX, x_scale, dA, dB, scale, index, base, row_scale, col_scale, dY, workspace), 0, stream)
 
 
 NM_ALG_AUTO, NM_ALG_TILE128, NM_ALG_TILE256X128, NM_ALG_TILE256, NM_ALG_COUNT = range(5)

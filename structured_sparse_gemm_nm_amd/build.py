@@ -20,7 +20,7 @@ CAL_LIB = os.path.join(HERE, "libnmcal.so")       # calibration loops for the be
 SOURCES = ["nm_api.hip", "nm_prune.hip", "nm_rows.hip", "nm_vw.hip", "nm_gemm.hip", "nm_gemm_f16.hip", "nm_gemm_bf16.hip",
            "nm_gemm_i8.hip",
            "nm_skinny_f16.hip", "nm_skinny_bf16.hip", "nm_skinny_i8.hip",
-           "nm_rowops.hip", "nm_heads.hip", "nm_logprobs.hip", "nm_w4.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip", "nm_w4_i8.hip", "nm_w4_i8_bf16.hip"]
+           "nm_rowops.hip", "nm_heads.hip", "nm_logprobs.hip", "nm_lora.hip", "nm_w4.hip", "nm_w4_f16.hip", "nm_w4_bf16.hip", "nm_w4_i8.hip", "nm_w4_i8_bf16.hip"]
 CALL_LIB = os.path.join(HERE, "_nmcall.so")       # operand checks and calls of the layer operators (Python extension)
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")

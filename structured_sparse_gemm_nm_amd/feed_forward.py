@@ -18,6 +18,9 @@ scale an output feature, so that the same integers serve both of the library's p
 The 8-bit activations of the two are the same; they differ in the 16-bit rounding
 of the few-token products alone.
 
+Each projection may have low-rank adapters beside it (``adapters.Adapters``), one a
+token: nm_lora adds them to the product, from the same 8-bit codes.
+
 Features must be multiples of 16. Weights are prepared with torch; every call runs
 in the library's kernels and may be captured into a graph. There is no backward
 pass: operands that require a gradient are refused while gradients are recorded.
@@ -162,22 +165,34 @@ class CompressedFeedForward:
             raise RuntimeError("the block has no backward pass: x and residual must not require a gradient "
                                "(detach them, or call it under torch.no_grad())")
 
-    def __call__(self, x, residual=None, few=None):
+    def _adapted(self, adapters, index, codes, scale, y, in_f, out_f):
+        if adapters is None:
+            return y
+        if (adapters.in_f, adapters.out_f, adapters.dtype) != (in_f, out_f, self.dtype):
+            raise ValueError("adapters must be %s, from %d to %d features" % (self.dtype, in_f, out_f))
+        out = y.values if y.row_scale is None else None
+        return Rows(adapters.add(codes, index, y, x_scale=scale, out=out))
+
+    def __call__(self, x, residual=None, few=None, adapters=None):
         """x: Rows or a 16-bit tensor (tokens x hidden); residual: 16-bit (tokens x hidden) or None.
         Returns the down product as Rows and the next residual h = x + residual.
-        few: which product to take; by default the 4-bit one up to FEW_TOKENS tokens."""
+        few: which product to take; by default the 4-bit one up to FEW_TOKENS tokens.
+        adapters: (index, gate_up, down): the tokens' adapters (int64, negative for none) and the ``Adapters`` of both
+        projections (None: the projection has none); their products come in 16 bits."""
         x = x if isinstance(x, Rows) else Rows(x)
         self._check(x, residual)
         n, device = x.values.shape[0], x.values.device
         few = n <= FEW_TOKENS if few is None else few
+        index, on_gate_up, on_down = adapters or (None, None, None)
         codes = torch.empty((n, self.hidden), dtype=torch.int8, device=device)
         scale = torch.empty((n,), device=device)
         h = torch.empty((n, self.hidden), dtype=self.dtype, device=device)
         nm_rmsnorm(self._rows("rmsnorm", n, self.hidden, x), x.values, self.gamma, codes, y_scale=scale, residual=residual,
                    h=h, row_scale=x.row_scale, col_scale=x.col_scale)
-        y = self.gate_up.product(codes, scale, few)
+        y = self._adapted(on_gate_up, index, codes, scale, self.gate_up.product(codes, scale, few), self.hidden, 2 * self.inner)
         inner = torch.empty((n, self.inner), dtype=torch.int8, device=device)
         inner_scale = torch.empty((n,), device=device)
         nm_swiglu(self._rows("swiglu", n, self.inner, y), y.values, inner, y_scale=inner_scale, row_scale=y.row_scale,
                   col_scale=y.col_scale)
-        return self.down.product(inner, inner_scale, few), h
+        y = self.down.product(inner, inner_scale, few)
+        return self._adapted(on_down, index, inner, inner_scale, y, self.inner, self.hidden), h
