@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_kernel(HeadArgs A) {
 // in LDS in their order and written out, and heads_gain_kernel adds the blocks'.
 template <int IO, bool HALVES, int G, bool GAIN>
 __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A) {
-  constexpr int U = 2;
+  constexpr int U = 3;
   const int j = threadIdx.x % G, group = threadIdx.x / G, step = HEAD_THREADS / G;
   HeadLane<HALVES> l;
   l.place(A, j);
@@ -201,12 +201,14 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A
 #pragma unroll
   for (int i = 0; i < 8; i++) dq[i] = dk[i] = 0.0f;
 
+  int64_t pos = A.positions[min((int64_t)blockIdx.x, A.rows - 1)];
   for (int64_t token = blockIdx.x; token < A.rows; token += gridDim.x) {
-    const int64_t pos = A.positions[token];
+    const int64_t now = pos;
     const uint8_t* const row = A.x + token * A.ldx * 2;
     const uint8_t* const drow = (const uint8_t*)(A.dy + token * A.lddy);
     uint16_t* const out = A.y + token * A.ldy;
-    if (pos < 0) {                                // no token: no gradient
+    pos = A.positions[min(token + gridDim.x, A.rows - 1)];
+    if (now < 0) {                                // no token: no gradient
       for (int h = group; h < A.heads; h += step)
         if (l.in) {
           *(u32x2*)(out + (int64_t)h * A.dim + l.lo) = u32x2{0, 0};
@@ -214,14 +216,16 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A
         }
       continue;
     }
-    l.angles(A, j, pos);
+    l.angles(A, j, now);
     for (int h0 = group; h0 < A.heads; h0 += U * step) {
       HeadRaw<false> xr[U], gr[U];
 #pragma unroll
       for (int n = 0; n < U; n++) {
-        const int h = min(h0 + n * step, A.heads - 1);
-        xr[n] = head_load<false>(A, row, h, l);
-        gr[n] = head_load<false>(A, drow, h, l);
+        const int h = h0 + n * step;
+        if (h < A.heads) {
+          xr[n] = head_load<false>(A, row, h, l);
+          gr[n] = head_load<false>(A, drow, h, l);
+        }
       }
 #pragma unroll
       for (int n = 0; n < U; n++) {
@@ -231,27 +235,30 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A
         head_values<IO, false>(u, xr[n], 1.0f, l.in);
         head_values<IO, false>(g, gr[n], 1.0f, l.in);
         if (h < A.normed) {
+          const bool query = h < A.q;
+          float w[8], uu = 0.0f, wu = 0.0f;
           l.turn(g, -1.0f);
-          float uu = 0.0f, wu = 0.0f;
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const float w = g[i] * (h < A.q ? gq[i] : gk[i]);
+            w[i] = g[i] * (query ? gq[i] : gk[i]);
             uu = __builtin_fmaf(u[i], u[i], uu);
-            wu = __builtin_fmaf(w, u[i], wu);
+            wu = __builtin_fmaf(w[i], u[i], wu);
           }
           uu = lane_sum<G>(uu);
           wu = lane_sum<G>(wu);
           const float f = 1.0f / __builtin_sqrtf(__builtin_fmaf(uu, A.rdim, A.eps));
           const float back = wu * A.rdim * f * f;
+          if constexpr (GAIN) {
+            if (query) {
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const float gu = g[i] * (u[i] * f);
-            if constexpr (GAIN) {
-              if (h < A.q) dq[i] += gu;
-              else dk[i] += gu;
+              for (int i = 0; i < 8; i++) dq[i] = __builtin_fmaf(g[i], u[i] * f, dq[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; i++) dk[i] = __builtin_fmaf(g[i], u[i] * f, dk[i]);
             }
-            g[i] = f * (g[i] * (h < A.q ? gq[i] : gk[i]) - u[i] * back);
           }
+#pragma unroll
+          for (int i = 0; i < 8; i++) g[i] = f * (w[i] - u[i] * back);
         }
         if (l.in) {
           uint16_t* const to = out + (int64_t)h * A.dim;
@@ -285,16 +292,22 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A
 
 // dgamma of 16 elements a block from the blocks' shares, in an order that the shape alone decides.
 template <int IO>
-__global__ void __launch_bounds__(256) heads_gain_kernel(const float* part, int shares, int dim, uint16_t* dq, uint16_t* dk) {
-  __shared__ double sums[256];
+__global__ void __launch_bounds__(1024) heads_gain_kernel(const float* part, int shares, int dim, uint16_t* dq, uint16_t* dk) {
+  __shared__ double sums[1024];
   const int e = blockIdx.x * 16 + threadIdx.x % 16, r = threadIdx.x / 16;
   double sum = 0.0;
-  if (e < 2 * dim)
-    for (int i = r; i < shares; i += 16) sum += (double)part[(int64_t)i * 2 * dim + e];
+  if (e < 2 * dim) {
+#pragma unroll 4
+    for (int i = 0; i < 16; i++)                  // 1024 shares at most
+      if (r + 64 * i < shares) sum += (double)part[(int64_t)(r + 64 * i) * 2 * dim + e];
+  }
   sums[threadIdx.x] = sum;
-  __syncthreads();
+  for (int half = 32; half > 0; half /= 2) {
+    __syncthreads();
+    if (r < half) sums[threadIdx.x] += sums[threadIdx.x + 16 * half];
+  }
   if (r > 0 || e >= 2 * dim) return;
-  for (int i = 1; i < 16; i++) sum += sums[i * 16 + threadIdx.x];
+  sum = sums[threadIdx.x];
   if (e < dim) dq[e] = to_bits16<IO>((float)sum);
   else if (dk) dk[e - dim] = to_bits16<IO>((float)sum);
 }
@@ -482,10 +495,10 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
   if (e == hipSuccess && gain) {
     const dim3 grid((unsigned)((2 * p.head_dim + 15) / 16));
     if (f16)
-      hipLaunchKernelGGL((heads_gain_kernel<DT_F16>), grid, dim3(256), 0, s, (const float*)a.part, blocks, p.head_dim,
+      hipLaunchKernelGGL((heads_gain_kernel<DT_F16>), grid, dim3(1024), 0, s, (const float*)a.part, blocks, p.head_dim,
                          (uint16_t*)d_grad_gamma_q, (uint16_t*)d_grad_gamma_k);
     else
-      hipLaunchKernelGGL((heads_gain_kernel<DT_BF16>), grid, dim3(256), 0, s, (const float*)a.part, blocks, p.head_dim,
+      hipLaunchKernelGGL((heads_gain_kernel<DT_BF16>), grid, dim3(1024), 0, s, (const float*)a.part, blocks, p.head_dim,
                          (uint16_t*)d_grad_gamma_q, (uint16_t*)d_grad_gamma_k);
     e = hipGetLastError();
   }

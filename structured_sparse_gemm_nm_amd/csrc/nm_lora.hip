@@ -53,6 +53,14 @@ __device__ __forceinline__ floatx4 lora_mma(typename LoraType<IO>::v a, typename
   else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+// What a wave's lanes wrote to LDS its other lanes read, and write over once all have
+// read: a wave's LDS operations keep their order, and the compiler keeps to it.
+__device__ __forceinline__ void lora_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // The adapters of a tile's tokens, one lane a token: its adapter, -1 for none, -2 for one
 // that does not exist, -3 behind the last token.
 __device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0) {
@@ -98,55 +106,93 @@ __device__ __forceinline__ u32x4 lora_codes(uint32_t lo, uint32_t hi) {
   return r;
 }
 
+// A wave's columns: the tokens of a group, in their order. Up to 16 tokens are their own
+// columns, so that what does not depend on their adapters need not wait for it.
+template <int NT> struct LoraColumns {
+  static constexpr bool OWN = NT == 1;
+  int* list;              // this wave's, in LDS
+  uint64_t group;
+  int count;              // columns that may be taken
+
+  __device__ __forceinline__ void set(int* l, uint64_t g, int64_t n) {
+    list = l;
+    group = g;
+    count = OWN ? (int)n : __popcll(g);
+    if constexpr (!OWN) {
+      const int lane = threadIdx.x & 63;
+      lora_lds_order();
+      if (g >> lane & 1)
+        list[__builtin_amdgcn_mbcnt_hi((uint32_t)(g >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)g, 0))] = lane;
+      lora_lds_order();
+    }
+  }
+  // whether a column holds one of the group's tokens, and its token (any of the tile's where it does not)
+  __device__ __forceinline__ bool has(int col) const { return col < count && (!OWN || (group >> col & 1)); }
+  __device__ __forceinline__ int token(int col) const {
+    const int c = min(col, count - 1);
+    return OWN ? c : list[c];
+  }
+};
+
 // t of one adapter's tokens, part blockIdx.x of k. A wave takes one tile of 16 ranks and,
 // LORA_KW at a time, its share of the part; the waves of a rank tile are added in LDS in
 // their order. The instruction's rows are ranks, its columns tokens.
 template <int IO, bool X8, int NT>
 __global__ void __launch_bounds__(64 * LORA_WAVES) lora_inner_kernel(LoraArgs A) {
   typedef typename LoraType<IO>::v v_t;
+  typedef LoraColumns<NT> cols_t;
+  constexpr int XS = X8 ? 2 : 4;
   __shared__ floatx4 red[LORA_WAVES][NT][64];
-  __shared__ int tokens[LORA_WAVES][LORA_TILE];
+  __shared__ int tokens[cols_t::OWN ? 1 : LORA_WAVES][LORA_TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
   const int mine = lora_named(A, tile0);
-  uint64_t left = __ballot(mine >= 0);
   const int rank_tiles = (A.rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
   const int rt = wave % across, part = wave / across, parts = LORA_WAVES / across;
+  const bool works = 16 * rt < A.rank;
+  auto first_k = [&](int i) { return (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW; };
 
+  u32x4 xv[NT][XS];
+  auto load_x = [&](const uint8_t* const (&xr)[NT], int64_t k0, int count) {
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+      if (16 * j < count) {
+#pragma unroll
+        for (int s = 0; s < XS; s++) xv[j][s] = lora_piece<X8 ? 1 : 2>(xr[j], k0 + (X8 ? 64 * s + 16 * q : 32 * s + 8 * q), A.k);
+      }
+  };
+  const uint8_t* xr[NT];
+  if constexpr (cols_t::OWN) {
+    xr[0] = A.x + min(l16, (int)A.n - 1) * A.ldx * (X8 ? 1 : 2);
+    if (works && first_k(0) < A.k) load_x(xr, first_k(0), 16);
+  }
+  uint64_t left = __ballot(mine >= 0);
   for (int d = 0, next = blockIdx.z; left; d++) {
     int adapter;
     const uint64_t group = lora_group(mine, left, adapter);
     if (d != next) continue;
     next += gridDim.z;
-    const int count = __popcll(group);
-    // columns to tokens, a copy a wave
-    if (group >> lane & 1) tokens[wave][__builtin_amdgcn_mbcnt_hi((uint32_t)(group >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)group, 0))] = lane;
-    __syncthreads();
+    cols_t cols;
+    cols.set(tokens[cols_t::OWN ? 0 : wave], group, A.n);
     const uint8_t* const ar = (const uint8_t*)(A.a + ((int64_t)adapter * A.rank + min(16 * rt + l16, A.rank - 1)) * A.lda);
-    const uint8_t* xr[NT];
+    if constexpr (!cols_t::OWN) {
 #pragma unroll
-    for (int j = 0; j < NT; j++)
-      xr[j] = A.x + (tile0 + tokens[wave][min(16 * j + l16, count - 1)]) * A.ldx * (X8 ? 1 : 2);
+      for (int j = 0; j < NT; j++) xr[j] = A.x + (tile0 + cols.token(16 * j + l16)) * A.ldx * (X8 ? 1 : 2);
+    }
     floatx4 acc[NT];
 #pragma unroll
     for (int j = 0; j < NT; j++) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (16 * rt < A.rank) {
+    if (works) {
       for (int i = 0; i < A.loops; i++) {
-        const int64_t k0 = (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW;
+        const int64_t k0 = first_k(i);
         if (k0 >= A.k) break;
-        u32x4 av[4], xv[NT][X8 ? 2 : 4];
+        u32x4 av[4];
 #pragma unroll
         for (int s = 0; s < 4; s++) av[s] = lora_piece<2>(ar, k0 + (X8 ? 64 * (s / 2) + 16 * q + 8 * (s % 2) : 32 * s + 8 * q), A.k);
+        if (!cols_t::OWN || i > 0 || d > (int)blockIdx.z) load_x(xr, k0, cols.count);
 #pragma unroll
         for (int j = 0; j < NT; j++)
-          if (16 * j < count) {
-#pragma unroll
-            for (int s = 0; s < (X8 ? 2 : 4); s++)
-              xv[j][s] = lora_piece<X8 ? 1 : 2>(xr[j], k0 + (X8 ? 64 * s + 16 * q : 32 * s + 8 * q), A.k);
-          }
-#pragma unroll
-        for (int j = 0; j < NT; j++)
-          if (16 * j < count) {
+          if (16 * j < cols.count) {
 #pragma unroll
             for (int s = 0; s < 4; s++) {
               u32x4 b;
@@ -164,8 +210,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_inner_kernel(LoraArgs A)
       const int r = u % across, j = u / across, col = 16 * j + l16, rank = 16 * r + 4 * q;
       floatx4 v = red[r][j][lane];
       for (int w = 1; w < parts; w++) v += red[r + w * across][j][lane];
-      if (col < count && rank < A.rank)
-        *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + tile0 + tokens[wave][col]) * A.rank + rank) = v;
+      if (cols.has(col) && rank < A.rank)
+        *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + tile0 + cols.token(col)) * A.rank + rank) = v;
     }
     __syncthreads();
   }
@@ -181,28 +227,69 @@ __global__ void __launch_bounds__(64 * LORA_WAVES) lora_inner_kernel(LoraArgs A)
 template <int IO, bool ACC, int SETS, int NT>
 __global__ void __launch_bounds__(256) lora_outer_kernel(LoraArgs A) {
   typedef typename LoraType<IO>::v v_t;
+  typedef LoraColumns<NT> cols_t;
   constexpr int NS = SETS == 0 ? 1 : SETS;
-  constexpr int RS = (SETS == 0 ? 16 : 32 * SETS) + 4;    // floats a token's t in LDS: 16 tokens on distinct banks
+  constexpr int PER = (SETS == 0 ? 16 : 32 * SETS) / 4;   // threads that bring a token's t
+  constexpr int RS = 4 * PER + 4;                         // floats of it in LDS: 16 tokens on distinct banks
+  constexpr int BQ = ACC ? 4 : 2;                         // pieces of 16 bytes a lane's outputs take of the base
   __shared__ float ts[16 * NT][RS];
-  __shared__ uint32_t most[16 * NT];
-  __shared__ int tokens[LORA_TILE];
+  __shared__ float most[16 * NT];
+  __shared__ int tokens[cols_t::OWN ? 1 : 4][LORA_TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
   const int64_t f0 = (int64_t)blockIdx.x * LORA_FEATURES + 64 * wave;
+  const bool all = f0 + 64 <= A.m;                        // the wave's outputs are whole
   const int mine = lora_named(A, tile0);
-  uint64_t left = __ballot(mine >= -2);
   const int chunks = A.rank / 8;
 
+  // what y adds to, as it lies in memory: outputs 32 h + 8 q .. + 7, h = 0, 1
+  u32x4 base[NT][BQ];
+  floatx4 cs[ACC ? 4 : 1];
+  float xs[NT], rs[NT];
+  int64_t token[NT];
+  auto load_base = [&](int j) {
+    xs[j] = A.x_scale ? A.x_scale[token[j]] : 1.0f;
+    if constexpr (ACC) rs[j] = A.row_scale[token[j]];
+    if (!all) return;
+    const uint8_t* p = A.base + (token[j] * A.ldc + f0 + 8 * q) * (ACC ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < BQ; i++) base[j][i] = *(const u32x4*)(p + (ACC ? 128 * (i / 2) + 16 * (i % 2) : 64 * i));
+  };
+  // one of the lane's 16 outputs of column j
+  auto value = [&](int j, int h, int e) -> float {
+    if (all) {
+      if constexpr (ACC) {
+        const uint32_t c = base[j][2 * h + e / 4][e % 4];
+        return (float)(int32_t)c * rs[j] * cs[2 * h + e / 4][e % 4];
+      } else {
+        return from_bits16<IO>((uint16_t)(base[j][h][e / 2] >> (16 * (e % 2))));
+      }
+    }
+    const int64_t out = f0 + 32 * h + 8 * q + e;
+    if (out >= A.m) return 0.0f;
+    if constexpr (ACC) return (float)((const int32_t*)A.base)[token[j] * A.ldc + out] * rs[j] * A.col_scale[out];
+    else return from_bits16<IO>(((const uint16_t*)A.base)[token[j] * A.ldc + out]);
+  };
+  if constexpr (ACC) {
+    if (all) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) cs[i] = *(const floatx4*)(A.col_scale + f0 + 8 * q + 32 * (i / 2) + 4 * (i % 2));
+    }
+  }
+  if constexpr (cols_t::OWN) {
+    token[0] = min(l16, (int)A.n - 1);
+    load_base(0);
+  }
+
+  uint64_t left = __ballot(mine >= -2);
   for (int d = 0, next = blockIdx.z; left; d++) {
     int adapter;
     const uint64_t group = lora_group(mine, left, adapter);
     if (d != next) continue;
     next += gridDim.z;
     if (adapter == -1 && A.in_place) continue;
-    const int count = __popcll(group);
-    __syncthreads();
-    if (wave == 0 && (group >> lane & 1))
-      tokens[__builtin_amdgcn_mbcnt_hi((uint32_t)(group >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)group, 0))] = lane;
+    cols_t cols;
+    cols.set(tokens[cols_t::OWN ? 0 : wave], group, A.n);
     // B's pieces: chunk 4 s + q (up to 16 ranks: q % 2) of the lane's output row
     v_t bv[NS][4];
 #pragma unroll
@@ -218,71 +305,57 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(LoraArgs A) {
       }
     }
     const float sa = adapter >= 0 ? A.scale[adapter] : adapter == -1 ? 0.0f : __builtin_nanf("");
-    for (int i = threadIdx.x; i < 16 * NT; i += 256) most[i] = 0;
-    __syncthreads();                            // tokens and most are there
-    if (adapter >= 0) {
-      const int per = (SETS == 0 ? 16 : 32 * SETS) / 4;
-      for (int e = threadIdx.x; e < 16 * NT * per; e += 256) {
-        const int j = e / per, r = e % per * 4;
-        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (j < count && r < A.rank) {
-          const float* p = A.t + (tile0 + tokens[j]) * A.rank + r;
-          for (int s = 0; s < A.splits; s++) v += *(const floatx4*)(p + (int64_t)s * A.n * A.rank);
-          if constexpr (IO == DT_F16) {
-            uint32_t top = 0;
+    if constexpr (!cols_t::OWN) {
 #pragma unroll
-            for (int i = 0; i < 4; i++) top = max(top, __builtin_bit_cast(uint32_t, (float)v[i]) & 0x7FFFFFFFu);
-            atomicMax(&most[j], top);           // a maximum: its order does not matter
+      for (int j = 0; j < NT; j++)
+        if (16 * j < cols.count) {
+          token[j] = tile0 + cols.token(16 * j + l16);
+          load_base(j);
+        }
+    }
+    if (adapter >= 0) {
+      // t: the parts of k in their order
+#pragma unroll 1
+      for (int e = threadIdx.x; e < 16 * NT * PER; e += 256) {
+        const int j = e / PER, r = e % PER * 4;
+        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (cols.has(j) && r < A.rank) {
+          const float* p = A.t + (tile0 + cols.token(j)) * A.rank + r;
+          for (int s = 0; s < A.splits; s += 4) {
+            floatx4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = *(const floatx4*)(p + (int64_t)min(s + i, A.splits - 1) * A.n * A.rank);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              if (s + i < A.splits) v += w[i];
           }
         }
         *(floatx4*)&ts[j][r] = v;
+        if constexpr (IO == DT_F16) {
+          float top = 0.0f;                       // a NaN is not among them; it stays in t
+#pragma unroll
+          for (int i = 0; i < 4; i++) top = fmaxf(top, __builtin_fabsf(v[i]));
+#pragma unroll
+          for (int off = 1; off < PER; off *= 2) top = fmaxf(top, __shfl_xor(top, off));
+          if (r == 0) most[j] = top;
+        }
       }
       __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < NT; j++) {
-      if (16 * j >= count) break;
-      const int col = 16 * j + l16;
-      const bool there = col < count;
-      const int64_t token = tile0 + tokens[min(col, count - 1)];
-      // what y adds to: two pieces of eight
+      if (16 * j >= cols.count) break;
       float v[2][8];
 #pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int64_t out = f0 + 32 * h + 8 * q;
-        if constexpr (ACC) {
-          const int32_t* p = (const int32_t*)A.base + token * A.ldc;
-          const float rs = A.row_scale[token];
+      for (int h = 0; h < 2; h++)
 #pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            if (out + i + 4 <= A.m) {
-              const intx4 c = *(const intx4*)(p + out + i);
-              const floatx4 cs = *(const floatx4*)(A.col_scale + out + i);
-#pragma unroll
-              for (int e = 0; e < 4; e++) v[h][i + e] = (float)c[e] * rs * cs[e];
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; e++) v[h][i + e] = out + i + e < A.m ? (float)p[out + i + e] * rs * A.col_scale[out + i + e] : 0.0f;
-            }
-          }
-        } else {
-          const uint16_t* p = (const uint16_t*)A.base + token * A.ldc;
-          if (out + 8 <= A.m) {
-            const u32x4 c = *(const u32x4*)(p + out);
-#pragma unroll
-            for (int e = 0; e < 8; e++) v[h][e] = from_bits16<IO>((uint16_t)(c[e / 2] >> (16 * (e % 2))));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++) v[h][e] = out + e < A.m ? from_bits16<IO>(p[out + e]) : 0.0f;
-          }
-        }
-      }
+        for (int e = 0; e < 8; e++) v[h][e] = value(j, h, e);
       if (adapter >= 0) {
         // t in two parts, and the factor that they leave
-        float up = 1.0f, fac = sa * (A.x_scale ? A.x_scale[token] : 1.0f);
+        float up = 1.0f, fac = sa * xs[j];
         if constexpr (IO == DT_F16) {
           // the largest below 1: times 2^-e with e its exponent's distance; not for 0, infinities and NaN
-          const int e = (int)(most[16 * j + l16] >> 23) - 126;
+          const int e = (int)(__builtin_bit_cast(uint32_t, most[16 * j + l16]) >> 23) - 126;
           if (e > -126 && e < 129) {
             up = __builtin_ldexpf(1.0f, -min(e, 120));        // 2^-127 is none; 2^8 f16 still holds
             fac *= __builtin_ldexpf(1.0f, min(e, 120));
@@ -325,15 +398,15 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(LoraArgs A) {
 #pragma unroll
         for (int e = 0; e < 8; e++) v[0][e] = v[1][e] = sa;
       }
-      if (!there) continue;
-      uint16_t* const yr = A.y + token * A.ldy;
+      if (!cols.has(16 * j + l16)) continue;
+      uint16_t* const yr = A.y + token[j] * A.ldy;
 #pragma unroll
       for (int h = 0; h < 2; h++) {
         const int64_t out = f0 + 32 * h + 8 * q;
         uint16_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) o[e] = to_bits16<IO>(v[h][e]);
-        if (out + 8 <= A.m) {
+        if (all) {
           u32x4 w;
 #pragma unroll
           for (int i = 0; i < 4; i++) w[i] = (uint32_t)o[2 * i] | (uint32_t)o[2 * i + 1] << 16;
@@ -345,6 +418,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(LoraArgs A) {
         }
       }
     }
+    __syncthreads();                              // t is read: the next group's may come
   }
 }
 
