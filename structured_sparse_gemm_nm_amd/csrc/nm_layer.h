@@ -36,6 +36,23 @@ template <int CTRL> __device__ __forceinline__ float lane_dpp(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
 }
 
+// f over the wave, the same in every lane: within 16 lanes without LDS, the four rows' results as scalars. Where a
+// single row's time is a sum of latencies, exchanges through LDS (130 clocks each) are most of it.
+template <typename F> __device__ __forceinline__ float wave_all(float v, F f) {
+  v = f(v, lane_dpp<0xB1>(v));
+  v = f(v, lane_dpp<0x4E>(v));
+  v = f(v, lane_dpp<0x141>(v));
+  v = f(v, lane_dpp<0x140>(v));
+  const int bits = __builtin_bit_cast(int, v);
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) r[i] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits, 16 * i));
+  return f(f(r[0], r[1]), f(r[2], r[3]));
+}
+__device__ __forceinline__ float wave_max(float v) { return wave_all(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float wave_min(float v) { return wave_all(v, [](float a, float b) { return fminf(a, b); }); }
+__device__ __forceinline__ float wave_sum(float v) { return wave_all(v, [](float a, float b) { return a + b; }); }
+
 // Sum over G neighbouring lanes (8, 16, 32 or 64), in each of them: neighbours,
 // pairs, the halves of 8 and of 16 mirrored, then across rows of 16.
 template <int G> __device__ __forceinline__ float lane_sum(float v) {

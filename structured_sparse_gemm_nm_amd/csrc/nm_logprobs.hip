@@ -3,9 +3,11 @@
 // include/nmsparse.h).
 //
 // The forward pass reads a row once: every thread keeps the largest logit it has
-// seen and, against it, the sum of exponentials and their weighted sum, and every
-// wave keeps a short list of candidates above a threshold that rises. Few long rows
-// are cut into slices, whose results a second kernel joins.
+// seen and, against it, the sum of exponentials and their weighted sum. Few long rows
+// are cut into slices, whose results a second kernel joins. The alternatives cost the
+// pass nothing: the K largest logits lie among the columns of threads (or of groups of
+// threads) whose largest is not below the K-th largest of such, and these columns
+// alone are read again.
 #include <float.h>
 #include <math.h>
 
@@ -17,14 +19,19 @@ struct nm_logprobs_plan {
   nm_logprobs_problem_t p;
   int slices;             // of a row
   int64_t slice;          // pieces of LP_V columns a slice
+  int threads, group;     // of a block; see LpArgs
 };
 
 namespace nm {
 
 constexpr int LP_V = 8;              // columns a thread takes at a time
 constexpr int LP_THREADS = 256;
+constexpr int LP_JOIN = 512;         // where the slices' alternatives are joined
+constexpr int LP_U = 2;              // pieces a thread takes at a time
 constexpr int LP_TOP = 32;           // most alternatives
+constexpr int LP_ROUNDS = 8;        // of 64 columns that a wave looks through together
 constexpr int LP_CAP = 128;          // candidates a wave holds
+constexpr int LP_CHUNKS = 2048;      // most groups of columns whose largest are kept for the alternatives
 constexpr int LP_MOST_SLICES = 64;
 constexpr int64_t LP_LONGEST = 1 << 17;   // columns a slice: a thread's chain of sums stays under 64 pieces
 
@@ -41,9 +48,10 @@ struct LpArgs {
   float* top_logprob;
   int64_t* top_index;
   floatx4* part;          // rows x slices: largest, sum, weighted sum
-  uint64_t* keys;         // rows x slices x top: the slices' candidates
+  float* largest;         // rows x chunks: the largest logits of the threads' groups
   int64_t rows, cols, ldx, slice;
   int slices, top;
+  int group;              // neighbouring threads whose columns are one chunk: 1, 4 or 16
   float scale, scale2;    // scale2 = scale * log2(e)
 };
 
@@ -99,13 +107,20 @@ struct LpTop {
   // of larger ones. Every lane of the wave takes part.
   __device__ __forceinline__ void compact() {
     const int lane = threadIdx.x & 63;
+    if (lane < 8 && count + lane < LP_CAP) buf[count + lane] = 0;       // they are read eight at a time
     lp_lds_order();
     const uint64_t a = lane < count ? buf[lane] : 0, b = lane + 64 < count ? buf[lane + 64] : 0;
     int ra = 0, rb = 0;
-    for (int i = 0; i < count; i++) {
-      const uint64_t k = buf[i];
-      ra += k > a;
-      rb += k > b;
+#pragma unroll 1
+    for (int i = 0; i < count; i += 8) {
+      uint64_t k[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) k[j] = buf[i + j];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        ra += k[j] > a;
+        rb += k[j] > b;
+      }
     }
     lp_lds_order();
     if (a && ra < top) buf[ra] = a;
@@ -131,38 +146,63 @@ struct LpTop {
       buf[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = key;
     count += __popcll(mask);
   }
-  // A first threshold from the lanes' largest logits: at least top of them reach the top-th largest.
-  __device__ __forceinline__ void estimate(float most) {
-    float* const f = (float*)buf;
-    const int lane = threadIdx.x & 63;
-    lp_lds_order();
-    f[lane] = most;
-    lp_lds_order();
-    int above = 0;
-    for (int i = 0; i < 64; i++) above += f[i] > most;
-    float v = above < top ? most : INFINITY;
-    for (int off = 32; off > 0; off >>= 1) v = fminf(v, __shfl_xor(v, off));
-    lp_lds_order();
-    value = v;
-  }
 };
 
-// The waves' lists joined by the first wave, whose list then holds the result. Every
-// thread of the block takes part.
-__device__ __forceinline__ void lp_top_join(LpTop& t, uint64_t (*lists)[LP_CAP]) {
-  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  t.compact();
-  if (waves == 1) return;
-  if (lane >= t.count && lane < LP_TOP) t.buf[lane] = 0;
-  __syncthreads();
-  if (wave == 0) {
-    for (int w = 1; w < waves; w += 2) {
-      const int from = w + lane / LP_TOP, at = lane % LP_TOP;
-      const uint64_t key = from < waves ? lists[from][at] : 0;
-      t.add(key, key != 0);
-    }
-    t.compact();
+// The top-th largest of the lanes' values (-infinity where there are fewer), by the
+// same counting; buf holds 64 floats of this wave, in LDS.
+__device__ __forceinline__ float lp_nth(float most, int top, float* buf) {
+  const int lane = threadIdx.x & 63;
+  lp_lds_order();
+  buf[lane] = most;
+  lp_lds_order();
+  int above = 0;
+#pragma unroll 4
+  for (int i = 0; i < 64; i += 4) {
+    const floatx4 o = *(const floatx4*)(buf + i);
+    above += (o[0] > most) + (o[1] > most) + (o[2] > most) + (o[3] > most);
   }
+  const float v = wave_min(above < top ? most : INFINITY);
+  lp_lds_order();
+  return v;
+}
+
+// The waves' lists joined by the first wave, whose list then holds the result. Every
+// thread of the block takes part. Lists that fit one are put behind each other and
+// ranked once; longer ones are first cut to their own largest.
+template <int W>
+__device__ __forceinline__ void lp_top_join(LpTop& t, uint64_t (*lists)[LP_CAP], int* counts) {
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (waves > 1) {
+    if (lane == 0) counts[wave] = t.count;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+      const int c = i < waves ? counts[i] : 0;
+      before += i < wave ? c : 0;
+      all += c;
+    }
+    if (all <= LP_CAP) {
+      if (wave > 0) {
+        for (int i = lane; i < t.count; i += 64) lists[0][before + i] = t.buf[i];
+      }
+      __syncthreads();
+      t.count = all;
+    } else {
+      t.compact();
+      if (lane >= t.count && lane < LP_TOP) t.buf[lane] = 0;
+      __syncthreads();
+      if (wave == 0) {
+#pragma unroll 1
+        for (int w = 1; w < waves; w += 2) {
+          const int from = w + lane / LP_TOP, at = lane % LP_TOP;
+          const uint64_t key = from < waves ? lists[from][at] : 0;
+          t.add(key, key != 0);
+        }
+      }
+    }
+  }
+  if (wave == 0) t.compact();
 }
 
 // ---- the running sums ----------------------------------------------------------
@@ -187,25 +227,29 @@ __device__ __forceinline__ float lp_max3(float a, float b, float c) {
 }
 
 // Over the block; every thread takes part and has the result.
+template <int W>
 __device__ __forceinline__ LpSum lp_join(LpSum t, float scale2) {
-  __shared__ floatx4 part[LP_THREADS / 64];
-  float m = t.m;
-  for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  __shared__ floatx4 part[W];
+  float m = wave_max(t.m);
   lp_shift(t, m, scale2);
-  t.s = lane_sum<64>(t.s);
-  t.w = lane_sum<64>(t.w);
+  t.s = wave_sum(t.s);
+  t.w = wave_sum(t.w);
   const int waves = blockDim.x >> 6;
   if (waves == 1) return t;
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = floatx4{t.m, t.s, t.w, 0.0f};
   __syncthreads();
-  m = part[0][0];
-  for (int i = 1; i < waves; i++) m = fmaxf(m, part[i][0]);
+  floatx4 o[W];
+#pragma unroll
+  for (int i = 0; i < W; i++) o[i] = part[min(i, waves - 1)];
+#pragma unroll
+  for (int i = 0; i < W; i++) m = fmaxf(m, o[i][0]);
   LpSum r = {m, 0.0f, 0.0f};
-  for (int i = 0; i < waves; i++) {
-    LpSum o = {part[i][0], part[i][1], part[i][2]};
-    lp_shift(o, m, scale2);
-    r.s += o.s;
-    r.w += o.w;
+#pragma unroll
+  for (int i = 0; i < W; i++) {
+    LpSum w = {o[i][0], o[i][1], o[i][2]};
+    lp_shift(w, m, scale2);
+    r.s += i < waves ? w.s : 0.0f;
+    r.w += i < waves ? w.w : 0.0f;
   }
   return r;
 }
@@ -252,10 +296,17 @@ __device__ __forceinline__ void lp_values(float (&x)[LP_V], const LpRaw<XT>& r, 
 }
 
 // ---- results --------------------------------------------------------------------
-// By a row's first thread: a row without any weight (every logit -infinity) has log
-// probabilities -infinity and entropy 0; a NaN or +infinity has made s NaN.
+// The logit of a row's token, 0 where it has none. Asked for early: two loads, one behind the other.
 template <int XT>
-__device__ __forceinline__ void lp_write(const LpArgs& A, int64_t row, const LpSum& t) {
+__device__ __forceinline__ float lp_given(const LpArgs& A, int64_t row, int64_t& token) {
+  token = A.logprob ? A.tokens[row] : -1;
+  if (token < 0 || token >= A.cols) return 0.0f;
+  return lp_one<XT>(A.x + row * A.ldx * LP_SIZE<XT>, A.col_scale, XT == LP_I32 ? A.row_scale[row] : 1.0f, token);
+}
+
+// By one thread of a row's: a row without any weight (every logit -infinity) has log
+// probabilities -infinity and entropy 0; a NaN or +infinity has made s NaN.
+__device__ __forceinline__ void lp_write(const LpArgs& A, int64_t row, const LpSum& t, int64_t token, float given) {
   const bool none = t.s == 0.0f;
   const float logs = logf(t.s);
   if (A.stats) {
@@ -264,14 +315,9 @@ __device__ __forceinline__ void lp_write(const LpArgs& A, int64_t row, const LpS
   }
   if (A.entropy) A.entropy[row] = none ? 0.0f : logs - A.scale * (t.w / t.s);
   if (A.logprob) {
-    const int64_t token = A.tokens[row];
-    float lp = 0.0f;
-    if (token >= A.cols) {
-      lp = NAN;
-    } else if (token >= 0) {
-      const float x = lp_one<XT>(A.x + row * A.ldx * LP_SIZE<XT>, A.col_scale, XT == LP_I32 ? A.row_scale[row] : 1.0f, token);
-      lp = none ? -INFINITY : (x - t.m) * A.scale - logs;
-    }
+    float lp = none ? -INFINITY : (given - t.m) * A.scale - logs;
+    if (token < 0) lp = 0.0f;
+    if (token >= A.cols) lp = NAN;
     A.logprob[row] = lp;
   }
 }
@@ -287,109 +333,220 @@ __device__ __forceinline__ void lp_write_top(const LpArgs& A, int64_t row, const
   A.top_index[row * A.top + lane] = known ? (int64_t)(uint32_t)~(uint32_t)key : -1;
 }
 
-// One block a slice of a row.
+// What the alternatives of a row need in LDS.
+template <int W> struct LpLists {
+  uint64_t keys[W][LP_CAP];
+  int chunks[W][LP_CHUNKS / W];
+  int counts[W];
+};
+
+// The alternatives of a row, from the largest logits of its chunks; every thread of the
+// block takes part, and the first wave has the result. A chunk is the columns of `group`
+// neighbouring threads of lp_kernel's block in a slice: group * LP_V in a row, and as
+// many again each `threads` pieces further on. At least top chunks reach the top-th
+// largest of a wave's lanes' (each the largest of some chunks), so the top largest logits
+// lie in chunks that reach it.
+template <int XT, int W>
+__device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const uint8_t* xr, float rs, const float* largest,
+                                                int threads, LpLists<W>& lds) {
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int per = threads / A.group, chunks = per * A.slices;
+  float most = -INFINITY;
+#pragma unroll 1
+  for (int i = lane; i < chunks; i += 8 * 64) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; u++) v[u] = largest[min(i + 64 * u, chunks - 1)];
+#pragma unroll
+    for (int u = 0; u < 8; u++) most = i + 64 * u < chunks ? fmaxf(most, v[u]) : most;
+  }
+  t.init(lds.keys[wave], A.top);
+  t.value = lp_nth(most, A.top, (float*)lds.keys[wave]);
+  // this wave's chunks
+  int* const list = lds.chunks[wave];
+  int count = 0;
+#pragma unroll 1
+  for (int b = 64 * wave + lane; b - lane < chunks; b += 4 * 64 * waves) {
+    float v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) v[u] = largest[min(b + 64 * waves * u, chunks - 1)];
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+      const int at = b + 64 * waves * u;
+      const bool holds = at < chunks && v[u] >= t.value;
+      const uint64_t mask = __ballot(holds);
+      if (holds) list[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = at;
+      count += __popcll(mask);
+    }
+  }
+  lp_lds_order();
+  // their columns, 64 at a time and LP_ROUNDS such rounds on their way; a chunk's rounds are taken for a power of two
+  const int rounds = (int)((A.slice + threads - 1) / threads), lw = 31 - __builtin_clz((unsigned)A.group * LP_V);
+  const int le = lw + (rounds > 1 ? 32 - __builtin_clz((unsigned)rounds - 1) : 0), total = count << le;
+  const int lp = 31 - __builtin_clz((unsigned)per);        // more slices than one have 256 threads
+  auto column = [&](int e, int& piece) -> int64_t {
+    const int chunk = e < total ? list[e >> le] : 0, in = e & ((1 << le) - 1), at = in & ((1 << lw) - 1);
+    const int first = A.slices == 1 ? 0 : chunk >> lp;
+    piece = (in >> lw) * threads + (chunk - (first << lp)) * A.group + at / LP_V;       // of its slice
+    return (first * A.slice + piece) * LP_V + at % LP_V;
+  };
+#pragma unroll 1
+  for (int b = lane; b - lane < total; b += LP_ROUNDS * 64) {
+    float x[LP_ROUNDS];
+    uint32_t hold = 0;
+#pragma unroll
+    for (int u = 0; u < LP_ROUNDS; u++) {
+      const int e = b + 64 * u;
+      int piece;
+      const int64_t c = column(e, piece);
+      const bool there = e < total && piece < A.slice && c < A.cols;
+      hold |= (uint32_t)there << u;
+      x[u] = lp_one<XT>(xr, A.col_scale, rs, there ? c : 0);       // no branch: all on their way
+    }
+#pragma unroll
+    for (int u = 0; u < LP_ROUNDS; u++)
+      if (!(x[u] >= t.value)) hold &= ~(1u << u);
+    while (__any(hold != 0)) {                             // one a lane at a time: few reach the bound
+      const int u = __builtin_ctz(hold | 1u << 31);
+      float v = x[0];
+#pragma unroll
+      for (int i = 1; i < LP_ROUNDS; i++) v = u == i ? x[i] : v;
+      int piece;
+      t.add(lp_key(v, (uint32_t)column(b + 64 * u, piece)), hold != 0);
+      hold &= hold - 1;
+    }
+  }
+  lp_top_join<W>(t, lds.keys, lds.counts);
+}
+
+// One block a slice of a row, LP_U pieces a thread at a time and the next ones on their way.
 template <int XT, bool ENT, bool TOP>
 __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
-  __shared__ uint64_t lists[TOP ? LP_THREADS / 64 : 1][LP_CAP];
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (block >= A.rows * A.slices) return;
-  const int64_t row = block / A.slices;
-  const int slice = (int)(block % A.slices);
+  const int64_t row = A.slices == 1 ? block : block / A.slices;
+  const int slice = (int)(block - row * A.slices);
   const uint8_t* const xr = A.x + row * A.ldx * LP_SIZE<XT>;
   const float rs = XT == LP_I32 ? A.row_scale[row] : 1.0f;
-  const int64_t begin = slice * A.slice, end = min(begin + A.slice, (A.cols + LP_V - 1) / LP_V);
+  const int begin = (int)(slice * A.slice), end = (int)min(begin + A.slice, (A.cols + LP_V - 1) / LP_V);
+  const int full = min(end, (int)(A.cols / LP_V));        // pieces that are whole
+  int64_t token = -1;
+  const float given = A.slices == 1 ? lp_given<XT>(A, row, token) : 0.0f;
 
   LpSum t = {-FLT_MAX, 0.0f, 0.0f};
-  LpTop top;
-  if constexpr (TOP) top.init(lists[threadIdx.x >> 6], A.top);
-  auto whole = [&](int64_t p) { return p < end && (p + 1) * LP_V <= A.cols; };
-
-  auto take = [&](const LpRaw<XT>& raw, int64_t p, bool first) {
-    float x[LP_V];
-    const int64_t c = p * LP_V;
-    if (whole(p)) {
-      lp_values<XT>(x, raw, rs);
-    } else {
+  auto take = [&](const LpRaw<XT> (&raw)[LP_U], int b) {
+    float x[LP_U][LP_V], most = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < LP_V; i++)
-        x[i] = p < end && c + i < A.cols ? lp_one<XT>(xr, A.col_scale, rs, c + i) : -INFINITY;
-    }
-    const float most = lp_max3(lp_max3(lp_max3(x[0], x[1], x[2]), x[3], x[4]), lp_max3(x[5], x[6], x[7]), x[7]);
-    if (most > t.m) lp_shift(t, most, A.scale2);
-    float s = 0.0f;
+    for (int u = 0; u < LP_U; u++) {
+      const int at = b + u * (int)blockDim.x + (int)threadIdx.x;
+      if (u > 0 && b + u * (int)blockDim.x >= end) break;
+      if (at < full) {
+        lp_values<XT>(x[u], raw[u], rs);
+      } else {
 #pragma unroll
-    for (int i = 0; i < LP_V; i++) {
-      const float d = x[i] - t.m, e = __builtin_amdgcn_exp2f(d * A.scale2);
-      s += e;
-      if constexpr (ENT) t.w = __builtin_fmaf(e, fmaxf(d, -FLT_MAX), t.w);   // e is 0 where d is infinite
-    }
-    t.s += s;
-    if constexpr (TOP) {
-      if (first) top.estimate(most);
-      if (__any(most >= top.value)) {
-#pragma unroll
-        for (int i = 0; i < LP_V; i++) {
-          const bool holds = x[i] >= top.value && p < end && c + i < A.cols;
-          if (__any(holds)) top.add(lp_key(x[i], (uint32_t)(c + i)), holds);
-        }
+        for (int i = 0; i < LP_V; i++)
+          x[u][i] = at < end && at * LP_V + i < A.cols ? lp_one<XT>(xr, A.col_scale, rs, at * LP_V + i) : -INFINITY;
       }
+#pragma unroll
+      for (int i = 0; i < LP_V; i += 2) most = lp_max3(most, x[u][i], x[u][i + 1]);
+    }
+    if (most > t.m) lp_shift(t, most, A.scale2);
+#pragma unroll
+    for (int u = 0; u < LP_U; u++) {
+      if (u > 0 && b + u * (int)blockDim.x >= end) break;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < LP_V; i++) {
+        const float d = x[u][i] - t.m, e = __builtin_amdgcn_exp2f(d * A.scale2);
+        s += e;
+        if constexpr (ENT) t.w = __builtin_fmaf(e, fmaxf(d, -FLT_MAX), t.w);   // e is 0 where d is infinite
+      }
+      t.s += s;
+    }
+  };
+  auto load = [&](LpRaw<XT> (&raw)[LP_U], int b) {
+#pragma unroll
+    for (int u = 0; u < LP_U; u++) {
+      const int at = b + u * (int)blockDim.x + (int)threadIdx.x;
+      lp_load<XT>(raw[u], xr, A.col_scale, (int64_t)at * LP_V, at < full, A.cols);
     }
   };
 
-  LpRaw<XT> raw, next;
-  int64_t p = begin + threadIdx.x;
-  lp_load<XT>(raw, xr, A.col_scale, p * LP_V, whole(p), A.cols);
-  for (int64_t b = begin; b < end; b += blockDim.x) {
-    p = b + threadIdx.x;
-    const int64_t q = p + blockDim.x;
-    lp_load<XT>(next, xr, A.col_scale, q * LP_V, whole(q), A.cols);
-    take(raw, p, b == begin);
-    raw = next;
+  LpRaw<XT> raw[LP_U], next[LP_U];
+  const int step = LP_U * (int)blockDim.x;
+  load(raw, begin);
+  for (int b = begin; b < end; b += step) {
+    if (b + step < end) load(next, b + step);
+    take(raw, b);
+#pragma unroll
+    for (int u = 0; u < LP_U; u++) raw[u] = next[u];
   }
 
-  t = lp_join(t, A.scale2);
-  if constexpr (TOP) lp_top_join(top, lists);
+  // -FLT_MAX stands for nothing but -infinity; a row's lowest logit may be it, and then
+  // counts as less than it is, which keeps the bound of the alternatives' chunks
+  float mine = t.m == -FLT_MAX ? -INFINITY : t.m;
   if (A.slices == 1) {
-    if (threadIdx.x == 0) lp_write<XT>(A, row, t);
     if constexpr (TOP) {
+      __shared__ LpLists<LP_THREADS / 64> lds;
+      __shared__ float largest[LP_THREADS];
+      largest[threadIdx.x] = mine;
+      t = lp_join<LP_THREADS / 64>(t, A.scale2);
+      __syncthreads();
+      LpTop top;
+      lp_alternatives<XT>(top, A, xr, rs, largest, blockDim.x, lds);
       if (threadIdx.x < 64) lp_write_top(A, row, t, top);
+    } else {
+      t = lp_join<LP_THREADS / 64>(t, A.scale2);
     }
+    if (threadIdx.x == blockDim.x - 1) lp_write(A, row, t, token, given);    // the first wave has the alternatives
   } else {
-    if (threadIdx.x == 0) A.part[block] = floatx4{t.m, t.s, t.w, 0.0f};
     if constexpr (TOP) {
-      if ((int)threadIdx.x < A.top) A.keys[block * A.top + threadIdx.x] = (int)threadIdx.x < top.count ? top.buf[threadIdx.x] : 0;
+      if (A.group >= 4) {
+        mine = fmaxf(mine, lane_dpp<0xB1>(mine));
+        mine = fmaxf(mine, lane_dpp<0x4E>(mine));
+      }
+      if (A.group >= 16) {
+        mine = fmaxf(mine, lane_dpp<0x141>(mine));
+        mine = fmaxf(mine, lane_dpp<0x140>(mine));
+      }
+      if (threadIdx.x % A.group == 0) A.largest[(block * LP_THREADS + threadIdx.x) / A.group] = mine;
     }
+    t = lp_join<LP_THREADS / 64>(t, A.scale2);
+    if (threadIdx.x == 0) A.part[block] = floatx4{t.m, t.s, t.w, 0.0f};
   }
 }
 
-// The slices of a row joined, one wave a row (a block without alternatives to join is one wave).
+// The slices of a row joined; one wave a row where there are no alternatives.
 template <int XT, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS) lp_join_kernel(LpArgs A) {
-  __shared__ uint64_t lists[TOP ? LP_THREADS / 64 : 1][LP_CAP];
+__global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
   const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= A.rows) return;
+  int64_t token;
+  const float given = lp_given<XT>(A, row, token);
   LpSum t = {-FLT_MAX, 0.0f, 0.0f};
   if ((int)threadIdx.x < A.slices) {
     const floatx4 v = A.part[row * A.slices + threadIdx.x];
     t = LpSum{v[0], v[1], v[2]};
   }
-  LpTop top;
   if constexpr (TOP) {
-    top.init(lists[threadIdx.x >> 6], A.top);
-    const int total = A.slices * A.top;
-    const uint64_t* const keys = A.keys + row * total;
-    for (int b = 0; b < total; b += blockDim.x) {         // the slices' first candidates before their second ones
-      const int i = b + threadIdx.x;
-      const uint64_t key = i < total ? keys[(i % A.slices) * A.top + i / A.slices] : 0;
-      top.add(key, key != 0);
-    }
-  }
-  t = lp_join(t, A.scale2);
-  if constexpr (TOP) lp_top_join(top, lists);
-  if (threadIdx.x == 0) lp_write<XT>(A, row, t);
-  if constexpr (TOP) {
+    __shared__ LpLists<LP_JOIN / 64> lds;
+    __shared__ float largest[LP_CHUNKS];
+    const int chunks = A.slices * (LP_THREADS / A.group);
+    const float* const from = A.largest + row * chunks;
+    float v[LP_CHUNKS / LP_JOIN];
+#pragma unroll
+    for (int i = 0; i < LP_CHUNKS / LP_JOIN; i++) v[i] = from[min((int)threadIdx.x + i * LP_JOIN, chunks - 1)];
+#pragma unroll
+    for (int i = 0; i < LP_CHUNKS / LP_JOIN; i++) largest[threadIdx.x + i * LP_JOIN] = v[i];
+    t = lp_join<LP_JOIN / 64>(t, A.scale2);
+    __syncthreads();
+    LpTop top;
+    lp_alternatives<XT>(top, A, A.x + row * A.ldx * LP_SIZE<XT>, XT == LP_I32 ? A.row_scale[row] : 1.0f, largest, LP_THREADS, lds);
     if (threadIdx.x < 64) lp_write_top(A, row, t, top);
+  } else {
+    t = lp_join<LP_JOIN / 64>(t, A.scale2);
   }
+  if (threadIdx.x == blockDim.x - 1) lp_write(A, row, t, token, given);      // the first wave has the alternatives
 }
 
 // dx_i = scale (g [i = t] - p_i (g + h (log p_i + H))), g and h the gradients of the
@@ -473,20 +630,16 @@ static dim3 lp_grid(int64_t blocks) {
 }
 
 template <int XT, bool ENT, bool TOP>
-hipError_t lp_go(const LpArgs& a, hipStream_t s) {
-  const int64_t waves = (a.slice + 63) / 64;
-  const dim3 threads((unsigned)(64 * (waves < LP_THREADS / 64 ? waves : LP_THREADS / 64)));
-  hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP>), lp_grid(a.rows * a.slices), threads, 0, s, a);
-  if (a.slices > 1) {
-    hipLaunchKernelGGL((lp_join_kernel<XT, TOP>), lp_grid(a.rows), dim3(TOP ? LP_THREADS : 64), 0, s, a);
-  }
+hipError_t lp_go(const LpArgs& a, int threads, hipStream_t s) {
+  hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP>), lp_grid(a.rows * a.slices), dim3((unsigned)threads), 0, s, a);
+  if (a.slices > 1) hipLaunchKernelGGL((lp_join_kernel<XT, TOP>), lp_grid(a.rows), dim3(TOP ? LP_JOIN : 64), 0, s, a);
   return hipGetLastError();
 }
 
 template <int XT>
-hipError_t lp_types(const LpArgs& a, hipStream_t s) {
-  if (a.top_index) return a.entropy ? lp_go<XT, true, true>(a, s) : lp_go<XT, false, true>(a, s);
-  return a.entropy ? lp_go<XT, true, false>(a, s) : lp_go<XT, false, false>(a, s);
+hipError_t lp_types(const LpArgs& a, int threads, hipStream_t s) {
+  if (a.top_index) return a.entropy ? lp_go<XT, true, true>(a, threads, s) : lp_go<XT, false, true>(a, threads, s);
+  return a.entropy ? lp_go<XT, true, false>(a, threads, s) : lp_go<XT, false, false>(a, threads, s);
 }
 
 template <int XT>
@@ -528,9 +681,11 @@ nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_pr
   if (n > LP_MOST_SLICES) n = LP_MOST_SLICES;
   const int64_t least = (p->cols + LP_LONGEST - 1) / LP_LONGEST;
   if (n < least) n = least;
-  pl->slice = ((rounds + n - 1) / n) * LP_THREADS;
-  if (n == 1) pl->slice = pieces;
+  pl->slice = n == 1 ? pieces : ((rounds + n - 1) / n) * LP_THREADS;
   pl->slices = (int)((pieces + pl->slice - 1) / pl->slice);
+  pl->threads = pl->slices > 1 || pieces >= LP_THREADS ? LP_THREADS : (int)((pieces + 63) / 64 * 64);
+  const int64_t all = (int64_t)pl->slices * pl->threads;
+  pl->group = all <= LP_CHUNKS ? 1 : all <= 4 * LP_CHUNKS ? 4 : 16;
   *plan = pl;
   return layer_fail(NM_OK, "");
 }
@@ -543,7 +698,7 @@ nm_status_t nm_logprobs_plan_destroy(nm_logprobs_plan_t plan) {
 nm_status_t nm_logprobs_workspace_size(nm_logprobs_plan_t plan, size_t* bytes) {
   if (!plan || !bytes) return layer_fail(NM_ERR_INVALID_ARG, "plan / bytes is NULL");
   const size_t parts = (size_t)plan->p.rows * plan->slices;
-  *bytes = plan->slices > 1 ? parts * (16 + 8 * (size_t)plan->p.top) : 0;
+  *bytes = plan->slices > 1 ? parts * (16 + (plan->p.top ? 4 * (size_t)(LP_THREADS / plan->group) : 0)) : 0;
   return NM_OK;
 }
 
@@ -579,22 +734,23 @@ nm_status_t nm_logprobs(nm_logprobs_plan_t plan, const void* dX, const float* d_
   a.top_index = d_top_index;
   if (plan->slices > 1) {
     a.part = (floatx4*)d_workspace;
-    a.keys = (uint64_t*)((uint8_t*)d_workspace + (size_t)p.rows * plan->slices * 16);
+    a.largest = (float*)((uint8_t*)d_workspace + (size_t)p.rows * plan->slices * 16);
   }
   a.rows = p.rows;
   a.cols = p.cols;
   a.ldx = p.ldx;
   a.slice = plan->slice;
   a.slices = plan->slices;
+  a.group = plan->group;
   a.top = p.top;
   a.scale = p.scale;
   a.scale2 = (float)((double)p.scale * 1.4426950408889634);
   hipStream_t s = (hipStream_t)stream;
   switch (p.type_x) {
-    case NM_F16: return layer_hip(lp_types<LP_F16>(a, s));
-    case NM_BF16: return layer_hip(lp_types<LP_BF16>(a, s));
-    case NM_F32: return layer_hip(lp_types<LP_F32>(a, s));
-    default: return layer_hip(lp_types<LP_I32>(a, s));
+    case NM_F16: return layer_hip(lp_types<LP_F16>(a, plan->threads, s));
+    case NM_BF16: return layer_hip(lp_types<LP_BF16>(a, plan->threads, s));
+    case NM_F32: return layer_hip(lp_types<LP_F32>(a, plan->threads, s));
+    default: return layer_hip(lp_types<LP_I32>(a, plan->threads, s));
   }
 }
 

@@ -114,7 +114,7 @@ def same(got, want, tol, what):
 
 
 SHAPES = [(1, 1), (3, 5), (2, 7), (5, 8), (4, 9), (33, 63), (70, 513), (9, 2048), (5, 2049), (1, 32003), (3, 50001), (1100, 2500),
-          (300, 9001), (1030, 4097), (2, 300000), (1, 1 << 20)]
+          (300, 9001), (1030, 4097), (2, 300000), (1, 1 << 20), (3, 1000003)]
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32", "i32"])
@@ -282,9 +282,9 @@ def test_tokens_that_start_off_the_16_bytes():
 
 
 def test_captured_and_on_another_stream():
-    s = inputs(3, 70001, "bf16", 12)
-    plan = nm.nm_logprobs_plan_init(3, 70001, dtype="bf16", top=20, ldx=70016, ldg=70016)
-    x = strided(s["x"], 70016, 0)[0]
+    s = inputs(3, 700001, "bf16", 12)
+    plan = nm.nm_logprobs_plan_init(3, 700001, dtype="bf16", top=20, ldx=700016, ldg=700016)
+    x = strided(s["x"], 700016, 0)[0]
     assert plan.workspace_bytes > 0
     out = [torch.empty(3, device="cuda"), torch.empty(3, device="cuda"), torch.empty((3, 2), device="cuda"),
            torch.empty((3, 20), device="cuda"), torch.empty((3, 20), dtype=torch.int64, device="cuda"),

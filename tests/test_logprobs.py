@@ -52,15 +52,15 @@ def test_fp32_is_for_logits_only():
 
 def test_workspace():
     assert plan().workspace_bytes == 0 and plan(top=5).workspace_bytes == 0
-    for kw in (dict(rows=1, cols=32000), dict(rows=16, cols=131072), dict(rows=1, cols=1 << 22), dict(rows=5000, cols=1 << 22)):
+    for kw in (dict(rows=1, cols=1 << 20), dict(rows=16, cols=1 << 20, dtype="f32"), dict(rows=1, cols=1 << 22), dict(rows=5000, cols=1 << 22)):
         a, b = plan(**kw).workspace_bytes, plan(top=9, **kw).workspace_bytes
-        assert a % (16 * kw["rows"]) == 0 and 1 < a // (16 * kw["rows"]) <= 64 and b == a // 16 * (16 + 72)
+        assert a % (16 * kw["rows"]) == 0 and 1 < a // (16 * kw["rows"]) <= 64 and b > a and (b - a) // (4 * kw["rows"]) <= 2048
     assert nm.lib().nm_logprobs_workspace_size(None, None) == nm.NM_ERR_INVALID_ARG
 
 
 def test_calls_refuse_bad_arguments():
     L, bad, odd = nm.lib(), nm.NM_ERR_INVALID_ARG, nm.NM_ERR_ALIGN
-    p, a, t, long, none = plan(), plan(dtype="i32"), plan(top=3), plan(rows=1, cols=32000), plan(rows=0)
+    p, a, t, long, none = plan(), plan(dtype="i32"), plan(top=3), plan(rows=1, cols=1 << 22), plan(rows=0)
     f, o = FAKE, ODD
     # x, row_scale, col_scale, tokens, logprob, entropy, stats, top_logprob, top_index, workspace, stream
     good = [f, None, None, f, f, f, f, None, None, None, None]
