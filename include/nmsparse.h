@@ -504,7 +504,7 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
  *  - A token's row depends on nothing but that token, its adapter and n.
  * There is no backward pass: adapters that are served are constants. */
 typedef struct {
-  int64_t m, n, k;          /* m <= 2^24, n <= 2^20, 1 <= k <= 2^20 */
+  int64_t m, n, k;          /* 8 <= m <= 2^24, n <= 2^20, 16 <= k <= 2^20 */
   int32_t adapters;         /* 1 to 2^20 */
   int32_t rank;             /* a multiple of 8, 8 to 128 */
   int32_t type_y;           /* y, A and B: NM_F16 or NM_BF16 */

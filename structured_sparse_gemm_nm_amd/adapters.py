@@ -29,8 +29,8 @@ class Adapters:
         self.out_f = b.shape[1]
         if b.shape != (self.count, self.out_f, rank) or scale.shape != (self.count,):
             raise ValueError("expected a (adapters x rank x in), b (adapters x out x rank) and scale (adapters)")
-        if not 1 <= rank <= 128 or not self.count or not self.in_f or not self.out_f:
-            raise ValueError("rank must be 1 to 128, and no dimension 0")
+        if not 1 <= rank <= 128 or not self.count or self.in_f < 16 or self.out_f < 8:
+            raise ValueError("rank must be 1 to 128, in at least 16 and out at least 8, and one adapter be given")
         if scale.dtype != torch.float32 or scale.device != a.device:
             raise ValueError("scale must be float32, with the adapters")
         a, b, pad = a.detach(), b.detach(), -rank % 8

@@ -113,11 +113,60 @@ def check_sparse_operands(asm_path):
     return bad
 
 
+# A matrix instruction's result is there a number of wait states after it; the
+# compiler fills them with s_nop. Where the result was stored to LDS in a block that
+# several others join, it has left them out, and LDS got what the registers held
+# before. The units below are read along every path for it.
+MATRIX_SOURCES = ("nm_lora.hip",)
+MATRIX_WAITS = 8                                   # of the 16x16 instructions
+
+
+def check_matrix_waits(asm_path, waits=MATRIX_WAITS):
+    """Instructions that use a 16x16 matrix instruction's result too early (empty list: sound)."""
+    import re
+
+    def regs(t):
+        out = set()
+        for kind, lo, hi in re.findall(r"\b([av])\[(\d+):(\d+)\]", t):
+            out |= {(kind, i) for i in range(int(lo), int(hi) + 1)}
+        return out | {(kind, int(i)) for kind, i in re.findall(r"\b([av])(\d+)\b", t)}
+
+    code, labels, bad = [], {}, []
+    for line in open(asm_path):
+        t = line.split(";")[0].strip()
+        if t.endswith(":"):
+            labels[t[:-1]] = len(code)
+        elif t and not t.startswith("."):
+            code.append(t)
+    for i, t in enumerate(code):
+        if not t.startswith(("v_mfma", "v_smfmac")):
+            continue
+        result, todo, seen = regs(t.split(",")[0]), [(i + 1, 0)], {}
+        while todo:
+            at, passed = todo.pop()
+            if at >= len(code) or passed >= waits or seen.get(at, waits) <= passed:
+                continue
+            seen[at] = passed
+            op, _, rest = code[at].partition(" ")
+            if op.startswith(("v_mfma", "v_smfmac")):
+                if regs(rest.split(",")[0]) & result:   # a chain of sums: the next one's result counts
+                    continue
+            elif regs(rest) & result:
+                bad.append("%s -> %s" % (t, code[at]))
+                continue
+            if op in ("s_branch",) or op.startswith("s_cbranch"):
+                if rest.strip() in labels:
+                    todo.append((labels[rest.strip()], passed + 1))
+            if op not in ("s_branch", "s_endpgm"):
+                todo.append((at + 1, passed + (int(rest) + 1 if op == "s_nop" else 1)))
+    return bad
+
+
 def _compile(src):
     stem = os.path.splitext(src)[0]
     obj = os.path.join(BUILD, stem + ".o")
     cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
-    if src in SPARSE_SOURCES:
+    if src in SPARSE_SOURCES + MATRIX_SOURCES:
         cmd += ["-save-temps=obj"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l)
@@ -129,6 +178,10 @@ def _compile(src):
         bad = check_sparse_operands(os.path.join(BUILD, "%s-hip-amdgcn-amd-amdhsa-%s.s" % (stem, ARCH)))
         if bad:
             raise RuntimeError("%s: sparse matrix instructions overwrite their operands: %s" % (src, "; ".join(bad[:5])))
+    if src in MATRIX_SOURCES:
+        bad = check_matrix_waits(os.path.join(BUILD, "%s-hip-amdgcn-amd-amdhsa-%s.s" % (stem, ARCH)))
+        if bad:
+            raise RuntimeError("%s: results of matrix instructions are used too early: %s" % (src, "; ".join(bad[:5])))
     return obj
 
 

@@ -22,9 +22,10 @@ struct nm_lora_plan {
 namespace nm {
 
 constexpr int LORA_TILE = 64;      // tokens that are sorted into adapters together: a wave's lanes
-constexpr int LORA_WAVES = 8;      // waves of the inner product's blocks
+constexpr int LORA_WAVES = 8;      // waves a block
 constexpr int LORA_KW = 128;       // k that a wave takes at a time
-constexpr int LORA_FEATURES = 256; // outputs a block of the outer product
+constexpr int LORA_FEATURES = 256; // outputs a block of the outer product, or twice as many
+constexpr int64_t LORA_MANY = 1 << 17; // outputs of all groups that are more than the CUs take at a time
 
 struct LoraArgs {
   const uint8_t* x;
@@ -70,28 +71,49 @@ __device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0) {
   return i < 0 ? -1 : i < A.adapters ? (int)i : -2;
 }
 
-// The tokens of the next adapter among `left`, which loses them; named is that adapter.
-__device__ __forceinline__ uint64_t lora_group(int mine, uint64_t& left, int& named) {
-  named = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-  const uint64_t group = __ballot(mine == named);
-  left &= ~group;
-  return group;
-}
+// The groups of a tile (the tokens of one adapter, or of none) that fall to one of gridDim.z
+// blocks: with a block for each token, the group that the token leads; with fewer, every
+// gridDim.z-th group in the order of their first tokens.
+struct LoraGroups {
+  int mine, d;
+  uint64_t left;
+  bool each;
 
-// Sixteen bytes of a row's elements from k on; those from `end` on are 0.
-template <int ES>
-__device__ __forceinline__ u32x4 lora_piece(const uint8_t* row, int64_t k, int64_t end) {
-  constexpr int E = 16 / ES;
-  if (k + E <= end) return *(const u32x4*)(row + k * ES);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < E; e++)
-    if (k + e < end) {
-      if constexpr (ES == 2) v[e / 2] |= (uint32_t)((const uint16_t*)row)[k + e] << (16 * (e % 2));
-      else v[e / 4] |= (uint32_t)row[k + e] << (8 * (e % 4));
+  // tokens: those to be taken
+  __device__ __forceinline__ void init(int m, uint64_t tokens, int64_t in_tile) {
+    mine = m;
+    left = tokens;
+    d = 0;
+    each = (int64_t)gridDim.z >= in_tile;
+    if (each) left = tokens >> blockIdx.z & 1 ? 1ull << blockIdx.z : 0;
+  }
+  __device__ __forceinline__ bool next(uint64_t& group, int& named) {
+    while (left) {
+      const int lead = __builtin_ctzll(left);
+      named = __builtin_amdgcn_readlane(mine, lead);
+      group = __ballot(mine == named);
+      left &= ~group;
+      if (each ? __builtin_ctzll(group) == lead : d++ % gridDim.z == blockIdx.z) return true;
     }
+    return false;
+  }
+};
+
+// Sixteen bytes at any address: those of a row's last elements start anywhere.
+struct __attribute__((packed, aligned(1))) LoraAny { u32x4 v; };
+__device__ __forceinline__ u32x4 lora_load(const void* p) { return ((const LoraAny*)p)->v; }
+
+// Eight 16-bit elements without the first `drop`, which become 0.
+__device__ __forceinline__ u32x4 lora_drop(u32x4 v, int drop) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) v[i] &= (2 * i >= drop ? 0xFFFFu : 0) | (2 * i + 1 >= drop ? 0xFFFF0000u : 0);
   return v;
 }
+
+// Between the matrix instructions and the first other use of their results: where the two
+// were in different blocks the compiler left out the wait states between them (LDS then got
+// sums without their last instructions). The build reads the unit for it.
+__device__ __forceinline__ void lora_settle(floatx4& v) { asm volatile("s_nop 15" : "+v"(v)); }
 
 // Eight codes of 8 bits as 16-bit values, exact in both types.
 template <int IO>
@@ -108,16 +130,15 @@ __device__ __forceinline__ u32x4 lora_codes(uint32_t lo, uint32_t hi) {
 
 // A wave's columns: the tokens of a group, in their order. Up to 16 tokens are their own
 // columns, so that what does not depend on their adapters need not wait for it.
-template <int NT> struct LoraColumns {
-  static constexpr bool OWN = NT == 1;
+template <bool OWN> struct LoraColumns {
   int* list;              // this wave's, in LDS
   uint64_t group;
-  int count;              // columns that may be taken
+  int count;              // columns that may hold one
 
-  __device__ __forceinline__ void set(int* l, uint64_t g, int64_t n) {
+  __device__ __forceinline__ void set(int* l, uint64_t g) {
     list = l;
     group = g;
-    count = OWN ? (int)n : __popcll(g);
+    count = OWN ? 16 : __popcll(g);
     if constexpr (!OWN) {
       const int lane = threadIdx.x & 63;
       lora_lds_order();
@@ -126,316 +147,347 @@ template <int NT> struct LoraColumns {
       lora_lds_order();
     }
   }
-  // whether a column holds one of the group's tokens, and its token (any of the tile's where it does not)
-  __device__ __forceinline__ bool has(int col) const { return col < count && (!OWN || (group >> col & 1)); }
+  // whether a column holds one of the group's tokens, and its token (another of the group where it does not)
+  __device__ __forceinline__ bool has(int col) const { return OWN ? group >> col & 1 : col < count; }
   __device__ __forceinline__ int token(int col) const {
-    const int c = min(col, count - 1);
-    return OWN ? c : list[c];
+    return OWN ? (has(col) ? col : __builtin_ctzll(group)) : list[min(col, count - 1)];
   }
 };
+
+template <int N> struct LoraCount { static constexpr int n = N; };
+template <int J, int XS> struct LoraStep { u32x4 a[4], x[J][XS]; };   // what LORA_KW k of J columns need
 
 // t of one adapter's tokens, part blockIdx.x of k. A wave takes one tile of 16 ranks and,
 // LORA_KW at a time, its share of the part; the waves of a rank tile are added in LDS in
 // their order. The instruction's rows are ranks, its columns tokens.
-template <int IO, bool X8, int NT>
-__global__ void __launch_bounds__(64 * LORA_WAVES) lora_inner_kernel(LoraArgs A) {
+template <int IO, bool X8, int NT, bool OWN>
+__global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs A) {
   typedef typename LoraType<IO>::v v_t;
-  typedef LoraColumns<NT> cols_t;
+  typedef LoraColumns<OWN> cols_t;
   constexpr int XS = X8 ? 2 : 4;
   __shared__ floatx4 red[LORA_WAVES][NT][64];
-  __shared__ int tokens[cols_t::OWN ? 1 : LORA_WAVES][LORA_TILE];
+  __shared__ int tokens[OWN ? 1 : LORA_WAVES][LORA_TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
   const int mine = lora_named(A, tile0);
   const int rank_tiles = (A.rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
   const int rt = wave % across, part = wave / across, parts = LORA_WAVES / across;
-  const bool works = 16 * rt < A.rank;
-  auto first_k = [&](int i) { return (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW; };
 
-  u32x4 xv[NT][XS];
-  auto load_x = [&](const uint8_t* const (&xr)[NT], int64_t k0, int count) {
-#pragma unroll
-    for (int j = 0; j < NT; j++)
-      if (16 * j < count) {
-#pragma unroll
-        for (int s = 0; s < XS; s++) xv[j][s] = lora_piece<X8 ? 1 : 2>(xr[j], k0 + (X8 ? 64 * s + 16 * q : 32 * s + 8 * q), A.k);
-      }
-  };
-  const uint8_t* xr[NT];
-  if constexpr (cols_t::OWN) {
-    xr[0] = A.x + min(l16, (int)A.n - 1) * A.ldx * (X8 ? 1 : 2);
-    if (works && first_k(0) < A.k) load_x(xr, first_k(0), 16);
-  }
-  uint64_t left = __ballot(mine >= 0);
-  for (int d = 0, next = blockIdx.z; left; d++) {
-    int adapter;
-    const uint64_t group = lora_group(mine, left, adapter);
-    if (d != next) continue;
-    next += gridDim.z;
+  LoraGroups groups;
+  groups.init(mine, __ballot(mine >= 0), min((int64_t)LORA_TILE, A.n - tile0));
+  uint64_t group;
+  int adapter;
+  while (groups.next(group, adapter)) {
     cols_t cols;
-    cols.set(tokens[cols_t::OWN ? 0 : wave], group, A.n);
+    cols.set(tokens[OWN ? 0 : wave], group);
     const uint8_t* const ar = (const uint8_t*)(A.a + ((int64_t)adapter * A.rank + min(16 * rt + l16, A.rank - 1)) * A.lda);
-    if constexpr (!cols_t::OWN) {
+    for (int c0 = 0; c0 < cols.count; c0 += 16 * NT) {
+      floatx4 acc[NT];
 #pragma unroll
-      for (int j = 0; j < NT; j++) xr[j] = A.x + (tile0 + cols.token(16 * j + l16)) * A.ldx * (X8 ? 1 : 2);
-    }
-    floatx4 acc[NT];
+      for (int j = 0; j < NT; j++) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      // J columns of 16 tokens
+      auto product = [&](auto J) {
+        const uint8_t* xr[J.n];
 #pragma unroll
-    for (int j = 0; j < NT; j++) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (works) {
-      for (int i = 0; i < A.loops; i++) {
-        const int64_t k0 = first_k(i);
-        if (k0 >= A.k) break;
-        u32x4 av[4];
+        for (int j = 0; j < J.n; j++) xr[j] = A.x + (tile0 + cols.token(c0 + 16 * j + l16)) * A.ldx * (X8 ? 1 : 2);
+        constexpr int JN = decltype(J)::n;
+        typedef LoraStep<JN, XS> step_t;
+        auto first_k = [&](int i) { return (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW; };
+        // what lies behind k is loaded from the row's last elements, and those that came before are dropped from A
+        auto load = [&](step_t& S, int64_t k0, bool whole) {
+          constexpr int E = X8 ? 16 : 8;          // elements of x in 16 bytes
 #pragma unroll
-        for (int s = 0; s < 4; s++) av[s] = lora_piece<2>(ar, k0 + (X8 ? 64 * (s / 2) + 16 * q + 8 * (s % 2) : 32 * s + 8 * q), A.k);
-        if (!cols_t::OWN || i > 0 || d > (int)blockIdx.z) load_x(xr, k0, cols.count);
+          for (int s = 0; s < XS; s++) {
+            const int64_t at = k0 + 4 * E * s + E * q, from = whole ? at : min(at, A.k - E);
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-          if (16 * j < cols.count) {
+            for (int h = 0; h < E / 8; h++) {
+              u32x4& a = S.a[E / 8 * s + h];
+              a = lora_load(ar + (from + 8 * h) * 2);
+              if (!whole) a = lora_drop(a, (int)min(at - from - 8 * h, (int64_t)8));
+            }
+#pragma unroll
+            for (int j = 0; j < JN; j++) S.x[j][s] = lora_load(xr[j] + from * (X8 ? 1 : 2));
+          }
+          __builtin_amdgcn_sched_barrier(0);      // all are on their way
+        };
+        auto multiply = [&](const step_t& S) {
+#pragma unroll
+          for (int j = 0; j < JN; j++)
 #pragma unroll
             for (int s = 0; s < 4; s++) {
               u32x4 b;
-              if constexpr (X8) b = lora_codes<IO>(xv[j][s / 2][2 * (s % 2)], xv[j][s / 2][2 * (s % 2) + 1]);
-              else b = xv[j][s];
-              acc[j] = lora_mma<IO>(__builtin_bit_cast(v_t, av[s]), __builtin_bit_cast(v_t, b), acc[j]);
+              if constexpr (X8) {
+                uint32_t lo = S.x[j][s / 2][2 * (s % 2)], hi = S.x[j][s / 2][2 * (s % 2) + 1];
+                asm volatile("" : "+v"(lo), "+v"(hi));          // not before they are needed: values are twice the registers
+                b = lora_codes<IO>(lo, hi);
+              } else {
+                b = S.x[j][s];
+              }
+              acc[j] = lora_mma<IO>(__builtin_bit_cast(v_t, S.a[s]), __builtin_bit_cast(v_t, b), acc[j]);
+            }
+        };
+        int steps = 0;                            // of the wave's, those that lie within k whole
+        while (steps < A.loops && first_k(steps) + LORA_KW <= A.k) steps++;
+        step_t S, N;
+        if (steps > 0) {
+          load(S, first_k(0), true);
+#pragma unroll 1
+          for (int i = 1; i < steps; i++) {
+            if constexpr (JN == 1) {
+              load(N, first_k(i), true);          // the next ones behind the present one's products
+              multiply(S);
+              S = N;
+            } else {
+              multiply(S);
+              load(S, first_k(i), true);
             }
           }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < NT; j++) red[wave][j][lane] = acc[j];
-    __syncthreads();
-    for (int u = wave; u < across * NT; u += LORA_WAVES) {
-      const int r = u % across, j = u / across, col = 16 * j + l16, rank = 16 * r + 4 * q;
-      floatx4 v = red[r][j][lane];
-      for (int w = 1; w < parts; w++) v += red[r + w * across][j][lane];
-      if (cols.has(col) && rank < A.rank)
-        *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + tile0 + cols.token(col)) * A.rank + rank) = v;
-    }
-    __syncthreads();
-  }
-}
-
-// y of one adapter's tokens (or of those without one), LORA_FEATURES outputs a block, 64 a
-// wave. The instruction's rows are outputs, its columns tokens, its k the ranks twice: t
-// goes in as two 16-bit parts, the second what the first left over, so that 16 to 22 bits of
-// it meet B (f16: against the token's largest, brought to 1 by a power of two, which f16
-// would not hold otherwise). Row 4 q + r of instruction f is output 32 (f / 2) + 8 q + 4 (f % 2)
-// + r: a lane ends with two pieces of eight outputs in a row, 16 bytes each.
-// SETS: chunks of eight ranks a lane takes; 0: up to 16 ranks, both parts in one instruction.
-template <int IO, bool ACC, int SETS, int NT>
-__global__ void __launch_bounds__(256) lora_outer_kernel(LoraArgs A) {
-  typedef typename LoraType<IO>::v v_t;
-  typedef LoraColumns<NT> cols_t;
-  constexpr int NS = SETS == 0 ? 1 : SETS;
-  constexpr int PER = (SETS == 0 ? 16 : 32 * SETS) / 4;   // threads that bring a token's t
-  constexpr int RS = 4 * PER + 4;                         // floats of it in LDS: 16 tokens on distinct banks
-  constexpr int BQ = ACC ? 4 : 2;                         // pieces of 16 bytes a lane's outputs take of the base
-  __shared__ float ts[16 * NT][RS];
-  __shared__ float most[16 * NT];
-  __shared__ int tokens[cols_t::OWN ? 1 : 4][LORA_TILE];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
-  const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
-  const int64_t f0 = (int64_t)blockIdx.x * LORA_FEATURES + 64 * wave;
-  const bool all = f0 + 64 <= A.m;                        // the wave's outputs are whole
-  const int mine = lora_named(A, tile0);
-  const int chunks = A.rank / 8;
-
-  // what y adds to, as it lies in memory: outputs 32 h + 8 q .. + 7, h = 0, 1
-  u32x4 base[NT][BQ];
-  floatx4 cs[ACC ? 4 : 1];
-  float xs[NT], rs[NT];
-  int64_t token[NT];
-  auto load_base = [&](int j) {
-    xs[j] = A.x_scale ? A.x_scale[token[j]] : 1.0f;
-    if constexpr (ACC) rs[j] = A.row_scale[token[j]];
-    if (!all) return;
-    const uint8_t* p = A.base + (token[j] * A.ldc + f0 + 8 * q) * (ACC ? 4 : 2);
-#pragma unroll
-    for (int i = 0; i < BQ; i++) base[j][i] = *(const u32x4*)(p + (ACC ? 128 * (i / 2) + 16 * (i % 2) : 64 * i));
-  };
-  // one of the lane's 16 outputs of column j
-  auto value = [&](int j, int h, int e) -> float {
-    if (all) {
-      if constexpr (ACC) {
-        const uint32_t c = base[j][2 * h + e / 4][e % 4];
-        return (float)(int32_t)c * rs[j] * cs[2 * h + e / 4][e % 4];
-      } else {
-        return from_bits16<IO>((uint16_t)(base[j][h][e / 2] >> (16 * (e % 2))));
-      }
-    }
-    const int64_t out = f0 + 32 * h + 8 * q + e;
-    if (out >= A.m) return 0.0f;
-    if constexpr (ACC) return (float)((const int32_t*)A.base)[token[j] * A.ldc + out] * rs[j] * A.col_scale[out];
-    else return from_bits16<IO>(((const uint16_t*)A.base)[token[j] * A.ldc + out]);
-  };
-  if constexpr (ACC) {
-    if (all) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) cs[i] = *(const floatx4*)(A.col_scale + f0 + 8 * q + 32 * (i / 2) + 4 * (i % 2));
-    }
-  }
-  if constexpr (cols_t::OWN) {
-    token[0] = min(l16, (int)A.n - 1);
-    load_base(0);
-  }
-
-  uint64_t left = __ballot(mine >= -2);
-  for (int d = 0, next = blockIdx.z; left; d++) {
-    int adapter;
-    const uint64_t group = lora_group(mine, left, adapter);
-    if (d != next) continue;
-    next += gridDim.z;
-    if (adapter == -1 && A.in_place) continue;
-    cols_t cols;
-    cols.set(tokens[cols_t::OWN ? 0 : wave], group, A.n);
-    // B's pieces: chunk 4 s + q (up to 16 ranks: q % 2) of the lane's output row
-    v_t bv[NS][4];
-#pragma unroll
-    for (int s = 0; s < NS; s++) {
-      const int chunk = SETS == 0 ? q % 2 : 4 * s + q;
-#pragma unroll
-      for (int f = 0; f < 4; f++) {
-        const int64_t out = f0 + 32 * (f / 2) + 8 * (l16 / 4) + 4 * (f % 2) + l16 % 4;
-        u32x4 v = {0, 0, 0, 0};
-        if (adapter >= 0 && chunk < chunks)
-          v = *(const u32x4*)(A.b + ((int64_t)adapter * A.m + min(out, A.m - 1)) * A.rank + 8 * chunk);
-        bv[s][f] = __builtin_bit_cast(v_t, v);
-      }
-    }
-    const float sa = adapter >= 0 ? A.scale[adapter] : adapter == -1 ? 0.0f : __builtin_nanf("");
-    if constexpr (!cols_t::OWN) {
-#pragma unroll
-      for (int j = 0; j < NT; j++)
-        if (16 * j < cols.count) {
-          token[j] = tile0 + cols.token(16 * j + l16);
-          load_base(j);
+          multiply(S);
         }
-    }
-    if (adapter >= 0) {
-      // t: the parts of k in their order
-#pragma unroll 1
-      for (int e = threadIdx.x; e < 16 * NT * PER; e += 256) {
-        const int j = e / PER, r = e % PER * 4;
-        floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (cols.has(j) && r < A.rank) {
-          const float* p = A.t + (tile0 + cols.token(j)) * A.rank + r;
-          for (int s = 0; s < A.splits; s += 4) {
-            floatx4 w[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) w[i] = *(const floatx4*)(p + (int64_t)min(s + i, A.splits - 1) * A.n * A.rank);
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              if (s + i < A.splits) v += w[i];
-          }
+        if (steps < A.loops && first_k(steps) < A.k) {
+          load(S, first_k(steps), false);
+          multiply(S);
         }
-        *(floatx4*)&ts[j][r] = v;
-        if constexpr (IO == DT_F16) {
-          float top = 0.0f;                       // a NaN is not among them; it stays in t
+      };
+      if (16 * rt < A.rank) {
+        if (NT == 1 || cols.count <= 16) product(LoraCount<1>());
+        else product(LoraCount<NT>());
+      }
 #pragma unroll
-          for (int i = 0; i < 4; i++) top = fmaxf(top, __builtin_fabsf(v[i]));
-#pragma unroll
-          for (int off = 1; off < PER; off *= 2) top = fmaxf(top, __shfl_xor(top, off));
-          if (r == 0) most[j] = top;
-        }
+      for (int j = 0; j < NT; j++) {
+        lora_settle(acc[j]);
+        red[wave][j][lane] = acc[j];
+      }
+      __syncthreads();
+      for (int u = wave; u < across * NT; u += LORA_WAVES) {
+        const int r = u % across, j = u / across, col = c0 + 16 * j + l16, rank = 16 * r + 4 * q;
+        floatx4 v = red[r][j][lane];
+        for (int w = 1; w < parts; w++) v += red[r + w * across][j][lane];
+        if (cols.has(col) && rank < A.rank)
+          *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + tile0 + cols.token(col)) * A.rank + rank) = v;
       }
       __syncthreads();
     }
+  }
+}
+
+// y of one adapter's tokens (or of those without one), LORA_FEATURES outputs a block, 32 a
+// wave. The instruction's rows are outputs, its columns tokens, its k the ranks twice: t
+// goes in as two 16-bit parts, the second what the first left over, so that 16 to 22 bits of
+// it meet B (f16: against the token's largest, brought to 1 by a power of two, which f16
+// would not hold otherwise). Row 4 q + r of instruction f is output 8 q + 4 f + r: a lane
+// ends with eight outputs in a row, 16 bytes.
+// SETS: chunks of eight ranks a lane takes; 0: up to 16 ranks, both parts in one instruction.
+template <int IO, bool ACC, int SETS, int NT, bool OWN, int FB>
+__global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs A) {
+  typedef typename LoraType<IO>::v v_t;
+  typedef LoraColumns<OWN> cols_t;
+  constexpr int THREADS = 64 * LORA_WAVES;
+  constexpr int NS = SETS == 0 ? 1 : SETS;
+  constexpr int RANKS = SETS == 0 ? 16 : 32 * SETS;
+  constexpr int PER = RANKS / 4;                          // threads that bring a token's t
+  constexpr int WS = 4;                                   // parts of t on their way together
+  constexpr int BQ = ACC ? 2 : 1;                         // pieces of 16 bytes a lane's outputs take of the base
+  __shared__ uint16_t ts[16 * NT][2 * RANKS + 8];         // both parts of t; 16 tokens lie on distinct banks
+  __shared__ float factor[16 * NT];
+  __shared__ int tokens[OWN ? 1 : LORA_WAVES][LORA_TILE];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
+  const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
+  const int64_t f0 = ((int64_t)blockIdx.x * LORA_WAVES + wave) * (32 * FB);
+  // A lane's eight outputs; behind the last output the last eight, of which it stores what is its own.
+  auto first_out = [&](int b, int of) { return min(f0 + 32 * b + 8 * of, A.m - 8); };
+  int64_t out[FB];
 #pragma unroll
-    for (int j = 0; j < NT; j++) {
-      if (16 * j >= cols.count) break;
-      float v[2][8];
+  for (int b = 0; b < FB; b++) out[b] = first_out(b, q);
+  const int mine = lora_named(A, tile0);
+  const int chunks = A.rank / 8;
+
+  floatx4 cs[FB][2];
+  if constexpr (ACC) {
 #pragma unroll
-      for (int h = 0; h < 2; h++)
+    for (int b = 0; b < FB; b++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) v[h][e] = value(j, h, e);
-      if (adapter >= 0) {
-        // t in two parts, and the factor that they leave
-        float up = 1.0f, fac = sa * xs[j];
-        if constexpr (IO == DT_F16) {
-          // the largest below 1: times 2^-e with e its exponent's distance; not for 0, infinities and NaN
-          const int e = (int)(__builtin_bit_cast(uint32_t, most[16 * j + l16]) >> 23) - 126;
-          if (e > -126 && e < 129) {
-            up = __builtin_ldexpf(1.0f, -min(e, 120));        // 2^-127 is none; 2^8 f16 still holds
-            fac *= __builtin_ldexpf(1.0f, min(e, 120));
-          }
+      for (int i = 0; i < 2; i++) cs[b][i] = __builtin_bit_cast(floatx4, lora_load(A.col_scale + out[b] + 4 * i));
+  }
+
+  LoraGroups groups;
+  groups.init(mine, __ballot(mine >= -2), min((int64_t)LORA_TILE, A.n - tile0));
+  uint64_t group;
+  int adapter;
+  while (groups.next(group, adapter)) {
+    if (adapter == -1 && A.in_place) continue;
+    cols_t cols;
+    cols.set(tokens[OWN ? 0 : wave], group);
+    const float sa = adapter >= 0 ? A.scale[adapter] : adapter == -1 ? 0.0f : __builtin_nanf("");
+    for (int c0 = 0; c0 < cols.count; c0 += 16 * NT) {
+      // t first: what is behind it is not waited for until it is in LDS
+      auto part = [&](int e, int s) {
+        const float* p = A.t + (tile0 + cols.token(c0 + e / PER)) * A.rank + min(e % PER * 4, A.rank - 4);
+        return *(const floatx4*)(p + (int64_t)min(s, A.splits - 1) * A.n * A.rank);
+      };
+      floatx4 w[WS];
+      float xs = 1.0f;
+      if (adapter >= 0 && (int)threadIdx.x < 16 * NT * PER) {
+#pragma unroll
+        for (int i = 0; i < WS; i++) w[i] = part(threadIdx.x, i);
+      }
+      // B's pieces: chunk 4 s + q (up to 16 ranks: q % 2) of the lane's output row
+      v_t bv[FB][NS][2];
+#pragma unroll
+      for (int s = 0; s < NS; s++) {
+        const int chunk = SETS == 0 ? q % 2 : 4 * s + q;
+#pragma unroll
+        for (int f = 0; f < 2 * FB; f++) {
+          const int64_t row = first_out(f / 2, l16 / 4) + 4 * (f % 2) + l16 % 4;
+          u32x4 v = {0, 0, 0, 0};
+          if (adapter >= 0 && chunk < chunks) v = *(const u32x4*)(A.b + ((int64_t)adapter * A.m + row) * A.rank + 8 * chunk);
+          bv[f / 2][s][f % 2] = __builtin_bit_cast(v_t, v);
         }
-        floatx4 acc[4];
+      }
+      // what y adds to, as it lies in memory
+      u32x4 base[FB][NT][BQ];
+      float rs[NT];
+      int token[NT];
+      bool in[NT];
 #pragma unroll
-        for (int f = 0; f < 4; f++) acc[f] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < NT; j++) {
+        in[j] = cols.has(c0 + 16 * j + l16);
+        token[j] = cols.token(c0 + 16 * j + l16);
+        rs[j] = ACC ? A.row_scale[tile0 + token[j]] : 1.0f;
+        const uint8_t* const p = A.base + (tile0 + token[j]) * A.ldc * (ACC ? 4 : 2);
 #pragma unroll
-        for (int s = 0; s < NS; s++) {
-          const float* p = &ts[16 * j + l16][8 * (SETS == 0 ? q % 2 : 4 * s + q)];
-          uint16_t hi[8], lo[8];
+        for (int b = 0; b < FB; b++)
+#pragma unroll
+          for (int i = 0; i < BQ; i++) base[b][j][i] = lora_load(p + out[b] * (ACC ? 4 : 2) + 16 * i);
+      }
+      if (adapter >= 0) {
+#pragma unroll 1
+        for (int e = threadIdx.x; e < 16 * NT * PER; e += THREADS) {
+          const int j = e / PER, r = e % PER * 4;
+          if (A.x_scale) xs = A.x_scale[tile0 + cols.token(c0 + j)];
+          floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int s = 0; s < A.splits; s += WS) {          // the parts of k in their order
+            if (e >= THREADS || s > 0) {
+#pragma unroll
+              for (int i = 0; i < WS; i++) w[i] = part(e, s + i);
+            }
+#pragma unroll
+            for (int i = 0; i < WS; i++)
+              if (s + i < A.splits) v += w[i];
+          }
+          if (r >= A.rank || !cols.has(c0 + j)) v = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+          float up = 1.0f, fac = sa * xs;
+          if constexpr (IO == DT_F16) {
+            // the token's largest below 1: times 2^-x with x its exponent's distance; not for 0, infinities and NaN
+            float top = 0.0f;                     // a NaN is not among them; it stays in t
+#pragma unroll
+            for (int i = 0; i < 4; i++) top = fmaxf(top, __builtin_fabsf(v[i]));
+#pragma unroll
+            for (int off = 1; off < PER; off *= 2) top = fmaxf(top, __shfl_xor(top, off));
+            const int x = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 126;
+            if (x > -126 && x < 129) {
+              up = __builtin_ldexpf(1.0f, -min(x, 120));      // 2^-127 is none; 2^8 f16 still holds
+              fac *= __builtin_ldexpf(1.0f, min(x, 120));
+            }
+          }
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            const float a = v[2 * i] * up, b = v[2 * i + 1] * up;
+            const uint16_t ha = to_bits16<IO>(a), hb = to_bits16<IO>(b);
+            hi[i] = (uint32_t)ha | (uint32_t)hb << 16;
+            lo[i] = (uint32_t)to_bits16<IO>(a - from_bits16<IO>(ha)) | (uint32_t)to_bits16<IO>(b - from_bits16<IO>(hb)) << 16;
+          }
+          *(u32x2*)&ts[j][r] = u32x2{hi[0], hi[1]};
+          *(u32x2*)&ts[j][RANKS + r] = u32x2{lo[0], lo[1]};
+          if (r == 0) factor[j] = fac;
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int j = 0; j < NT; j++) {
+        if (c0 + 16 * j >= cols.count) break;
+        const int64_t at = tile0 + token[j];
+        const uint16_t* const tj = ts[16 * j + l16];
+        const float fac = factor[16 * j + l16];
+#pragma unroll
+        for (int b = 0; b < FB; b++) {
+          float v[8];
 #pragma unroll
           for (int e = 0; e < 8; e++) {
-            const float w = p[e] * up;
-            hi[e] = to_bits16<IO>(w);
-            lo[e] = to_bits16<IO>(w - from_bits16<IO>(hi[e]));
+            if constexpr (ACC) {
+              const uint32_t c = base[b][j][e / 4][e % 4];
+              v[e] = (float)(int32_t)c * rs[j] * cs[b][e / 4][e % 4];
+            } else {
+              v[e] = from_bits16<IO>((uint16_t)(base[b][j][0][e / 2] >> (16 * (e % 2))));
+            }
           }
-          u32x4 hv, lv;
+          if (adapter >= 0) {
+            floatx4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-          for (int i = 0; i < 4; i++) {
-            hv[i] = (uint32_t)hi[2 * i] | (uint32_t)hi[2 * i + 1] << 16;
-            lv[i] = (uint32_t)lo[2 * i] | (uint32_t)lo[2 * i + 1] << 16;
+            for (int s = 0; s < NS; s++) {
+              const v_t first = *(const v_t*)(tj + (SETS == 0 ? 8 * q : 8 * (4 * s + q)));  // up to 16 ranks: q / 2 is the part
+#pragma unroll
+              for (int f = 0; f < 2; f++) acc[f] = lora_mma<IO>(bv[b][s][f], first, acc[f]);
+              if constexpr (SETS > 0) {
+                const v_t second = *(const v_t*)(tj + RANKS + 8 * (4 * s + q));
+#pragma unroll
+                for (int f = 0; f < 2; f++) acc[f] = lora_mma<IO>(bv[b][s][f], second, acc[f]);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = __builtin_fmaf(fac, acc[e / 4][e % 4], v[e]);
+          } else if (adapter == -2) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) v[e] = sa;
           }
-          if constexpr (SETS == 0) {
+          if (in[j]) {
+            uint16_t* const yr = A.y + at * A.ldy + out[b];
+            const int skip = (int)min(f0 + 32 * b + 8 * q - out[b], (int64_t)8);   // another lane's
+            u32x4 p;
 #pragma unroll
-            for (int i = 0; i < 4; i++) hv[i] = q < 2 ? hv[i] : lv[i];
-          }
+            for (int i = 0; i < 4; i++) p[i] = (uint32_t)to_bits16<IO>(v[2 * i]) | (uint32_t)to_bits16<IO>(v[2 * i + 1]) << 16;
+            if (skip == 0) {
+              ((LoraAny*)yr)->v = p;
+            } else {
 #pragma unroll
-          for (int f = 0; f < 4; f++) {
-            acc[f] = lora_mma<IO>(bv[s][f], __builtin_bit_cast(v_t, hv), acc[f]);
-            if constexpr (SETS > 0) acc[f] = lora_mma<IO>(bv[s][f], __builtin_bit_cast(v_t, lv), acc[f]);
+              for (int e = 0; e < 8; e++)
+                if (e >= skip) yr[e] = (uint16_t)(p[e / 2] >> (16 * (e % 2)));
+            }
           }
         }
-#pragma unroll
-        for (int f = 0; f < 4; f++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) v[f / 2][4 * (f % 2) + e] = __builtin_fmaf(fac, acc[f][e], v[f / 2][4 * (f % 2) + e]);
-      } else if (adapter == -2) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) v[0][e] = v[1][e] = sa;
       }
-      if (!cols.has(16 * j + l16)) continue;
-      uint16_t* const yr = A.y + token[j] * A.ldy;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const int64_t out = f0 + 32 * h + 8 * q;
-        uint16_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = to_bits16<IO>(v[h][e]);
-        if (all) {
-          u32x4 w;
-#pragma unroll
-          for (int i = 0; i < 4; i++) w[i] = (uint32_t)o[2 * i] | (uint32_t)o[2 * i + 1] << 16;
-          *(u32x4*)(yr + out) = w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; e++)
-            if (out + e < A.m) yr[out + e] = o[e];
-        }
-      }
+      __syncthreads();                            // t is read: the next may come
     }
-    __syncthreads();                              // t is read: the next group's may come
   }
 }
 
 template <int IO, bool X8>
 hipError_t lora_inner(const LoraArgs& a, const nm_lora_plan& pl, hipStream_t s) {
   const dim3 grid((unsigned)a.splits, (unsigned)pl.tiles, (unsigned)pl.slots_in);
-  if (a.n <= 16) hipLaunchKernelGGL((lora_inner_kernel<IO, X8, 1>), grid, dim3(64 * LORA_WAVES), 0, s, a);
-  else hipLaunchKernelGGL((lora_inner_kernel<IO, X8, 4>), grid, dim3(64 * LORA_WAVES), 0, s, a);
+  const dim3 threads(64 * LORA_WAVES);
+  if (a.n <= 16) hipLaunchKernelGGL((lora_inner_kernel<IO, X8, 1, true>), grid, threads, 0, s, a);
+  else if (a.n <= LORA_TILE) hipLaunchKernelGGL((lora_inner_kernel<IO, X8, 1, false>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((lora_inner_kernel<IO, X8, 4, false>), grid, threads, 0, s, a);
   return hipGetLastError();
 }
 
 template <int IO, bool ACC, int SETS>
 hipError_t lora_outer(const LoraArgs& a, const nm_lora_plan& pl, hipStream_t s) {
-  const dim3 grid((unsigned)((a.m + LORA_FEATURES - 1) / LORA_FEATURES), (unsigned)pl.tiles, (unsigned)pl.slots_out);
-  if (a.n <= 16) hipLaunchKernelGGL((lora_outer_kernel<IO, ACC, SETS, 1>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((lora_outer_kernel<IO, ACC, SETS, 4>), grid, dim3(256), 0, s, a);
-  return hipGetLastError();
+  auto go = [&](auto kernel, int outputs) {
+    const dim3 grid((unsigned)((a.m + outputs - 1) / outputs), (unsigned)pl.tiles, (unsigned)pl.slots_out);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * LORA_WAVES), 0, s, a);
+    return hipGetLastError();
+  };
+  if (a.n > LORA_TILE) return go(lora_outer_kernel<IO, ACC, SETS, 4, false, 1>, LORA_FEATURES);
+  if constexpr (SETS < 2) {
+    if (a.m * pl.slots_out > LORA_MANY) {
+      if (a.n <= 16) return go(lora_outer_kernel<IO, ACC, SETS, 1, true, 2>, 2 * LORA_FEATURES);
+      return go(lora_outer_kernel<IO, ACC, SETS, 1, false, 2>, 2 * LORA_FEATURES);
+    }
+  }
+  if (a.n <= 16) return go(lora_outer_kernel<IO, ACC, SETS, 1, true, 1>, LORA_FEATURES);
+  return go(lora_outer_kernel<IO, ACC, SETS, 1, false, 1>, LORA_FEATURES);
 }
 
 template <int IO>
@@ -449,8 +501,6 @@ hipError_t lora_go(const LoraArgs& a, const nm_lora_plan& pl, hipStream_t s) {
   if (r <= 64) return acc ? lora_outer<IO, true, 2>(a, pl, s) : lora_outer<IO, false, 2>(a, pl, s);
   return acc ? lora_outer<IO, true, 4>(a, pl, s) : lora_outer<IO, false, 4>(a, pl, s);
 }
-
-static bool lora_empty(const nm_lora_problem_t& p) { return p.n == 0 || p.m == 0; }
 
 }  // namespace nm
 
@@ -466,7 +516,7 @@ nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* p) 
   if (p->type_x != p->type_y && p->type_x != NM_I8) return layer_fail(NM_ERR_INVALID_ARG, "type_x must be type_y or NM_I8");
   if (p->type_base != p->type_y && p->type_base != NM_I32)
     return layer_fail(NM_ERR_INVALID_ARG, "type_base must be type_y or NM_I32");
-  if (p->m < 0 || p->n < 0 || p->k < 1) return layer_fail(NM_ERR_SHAPE, "m and n must be >= 0, k >= 1");
+  if (p->m < 8 || p->n < 0 || p->k < 16) return layer_fail(NM_ERR_SHAPE, "m must be >= 8, n >= 0, k >= 16");
   if (p->m > ((int64_t)1 << 24) || p->n > ((int64_t)1 << 20) || p->k > ((int64_t)1 << 20))
     return layer_fail(NM_ERR_SHAPE, "m must be <= 2^24, n and k <= 2^20");
   if (p->rank < 8 || p->rank > 128 || p->rank % 8) return layer_fail(NM_ERR_SHAPE, "rank must be a multiple of 8 from 8 to 128");
@@ -481,23 +531,22 @@ nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* p) 
   pl->p = *p;
   pl->tiles = (int)((p->n + LORA_TILE - 1) / LORA_TILE);
   const int64_t tile = p->n < LORA_TILE ? p->n : LORA_TILE, tiles = pl->tiles ? pl->tiles : 1;
-  // a block for each adapter that a tile can name, while that leaves the GPU room
-  auto slots = [&](int64_t most, int64_t blocks) {
-    int64_t want = 2048 / blocks;
-    if (want > most) want = most;
-    return (int)(want < 1 ? 1 : want);
+  // a block for each token of a tile while that are few, then fewer for its groups
+  auto slots = [&](int64_t blocks) {
+    if (blocks * tile <= 4096) return (int)tile;
+    const int64_t want = 1024 / blocks;
+    return (int)(want < 1 ? 1 : want > tile ? tile : want);
   };
   const int rank_tiles = (p->rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
   const int64_t step = (int64_t)LORA_KW * (LORA_WAVES / across), steps = (p->k + step - 1) / step;
-  const int64_t named = tile < p->adapters ? tile : p->adapters;
   int64_t splits = 1024 / tiles;
   if (splits > 16) splits = 16;
   if (splits > steps) splits = steps;
   if (splits < 1) splits = 1;
   pl->loops = (int)((steps + splits - 1) / splits);
   pl->splits = (int)((steps + pl->loops - 1) / pl->loops);
-  pl->slots_in = slots(named, tiles * pl->splits);
-  pl->slots_out = slots(tile < p->adapters + 2 ? tile : p->adapters + 2, tiles * ((p->m + LORA_FEATURES - 1) / LORA_FEATURES + 1));
+  pl->slots_in = slots(tiles * pl->splits);
+  pl->slots_out = slots(tiles * ((p->m + LORA_FEATURES - 1) / LORA_FEATURES + 1));
   *plan = pl;
   return layer_fail(NM_OK, "");
 }
@@ -510,7 +559,7 @@ nm_status_t nm_lora_plan_destroy(nm_lora_plan_t plan) {
 nm_status_t nm_lora_workspace_size(nm_lora_plan_t plan, size_t* bytes) {
   if (!plan || !bytes) return layer_fail(NM_ERR_INVALID_ARG, "plan / bytes is NULL");
   const nm_lora_problem_t& p = plan->p;
-  *bytes = lora_empty(p) ? 0 : (size_t)plan->splits * p.n * p.rank * sizeof(float);
+  *bytes = (size_t)plan->splits * p.n * p.rank * sizeof(float);
   return NM_OK;
 }
 
@@ -523,7 +572,7 @@ nm_status_t nm_lora(nm_lora_plan_t plan, const void* dX, const float* d_x_scale,
       !layer_aligned(d_col_scale, 16) || !layer_aligned(dY, 16) || !layer_aligned(d_workspace, 16) ||
       !layer_aligned(d_index, 8) || !layer_aligned(d_x_scale, 4) || !layer_aligned(d_scale, 4) || !layer_aligned(d_row_scale, 4))
     return layer_fail(NM_ERR_ALIGN, "matrices, d_col_scale and d_workspace must be 16-byte aligned, the others as their elements");
-  if (lora_empty(p)) return NM_OK;
+  if (p.n == 0) return NM_OK;
   if (!dX || !dA || !dB || !d_scale || !d_index || !d_base || !dY)
     return layer_fail(NM_ERR_INVALID_ARG, "dX / dA / dB / d_scale / d_index / d_base / dY is NULL");
   if (!d_workspace) return layer_fail(NM_ERR_INVALID_ARG, "d_workspace is NULL");
