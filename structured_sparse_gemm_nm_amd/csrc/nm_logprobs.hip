@@ -65,7 +65,7 @@ struct LpBackArgs {
   uint8_t* dx;
   int64_t rows, cols, ldx, ldg;
   int parts;              // blocks a row
-  float scale;
+  float scale, scale2;    // scale2 = scale * log2(e)
 };
 
 // ---- a wave's candidates -------------------------------------------------------
@@ -206,18 +206,29 @@ __device__ __forceinline__ void lp_top_join(LpTop& t, uint64_t (*lists)[LP_CAP],
 }
 
 // ---- the running sums ----------------------------------------------------------
-// s = sum exp(scale (x - m)), w = sum exp(scale (x - m)) (x - m); m starts at the lowest
-// value, so that no difference is that of two infinities.
+// Exponents are in base 2: of a logit x against the largest m, (x - m) scale2. That takes
+// two instructions, u = x scale2 - ms with ms = m scale2 rounded one, and its rounding is the
+// same for every logit: u is off by r = m scale2 - ms, which a fused multiply-add gives
+// exactly, and the sums are put right when m changes. From |m scale2| = 2^20 on r is too
+// large for that and the two instructions are taken.
+// s = sum 2^u, w = sum 2^u u; m starts at the lowest value, so that no difference is that of
+// two infinities.
 struct LpSum {
   float m, s, w;
+  float ms, r;            // where the sums are against ms, and else 0
 };
 
-// The sums against the larger m2.
-__device__ __forceinline__ void lp_shift(LpSum& t, float m2, float scale2) {
-  const float d = fmaxf(t.m - m2, -FLT_MAX), f = __builtin_amdgcn_exp2f(d * scale2);
+__device__ __forceinline__ bool lp_near(float ms) { return __builtin_fabsf(ms) < 0x1p20f; }
+
+// The sums against m2, the largest so far or m itself; against its rounded multiple where `fast` allows it.
+__device__ __forceinline__ void lp_shift(LpSum& t, float m2, float scale2, bool fast) {
+  const float ms2 = m2 * scale2, r2 = fast && lp_near(ms2) ? __builtin_fmaf(m2, scale2, -ms2) : 0.0f;
+  const float d = fmaxf((t.m - m2) * scale2, -FLT_MAX) + (r2 - t.r), f = __builtin_amdgcn_exp2f(d);
   t.s *= f;
   t.w = __builtin_fmaf(t.s, d, f * t.w);          // no product of a vast d with sums that f makes 0
   t.m = m2;
+  t.ms = ms2;
+  t.r = r2;
 }
 
 __device__ __forceinline__ float lp_max3(float a, float b, float c) {
@@ -231,7 +242,7 @@ template <int W>
 __device__ __forceinline__ LpSum lp_join(LpSum t, float scale2) {
   __shared__ floatx4 part[W];
   float m = wave_max(t.m);
-  lp_shift(t, m, scale2);
+  lp_shift(t, m, scale2, false);
   t.s = wave_sum(t.s);
   t.w = wave_sum(t.w);
   const int waves = blockDim.x >> 6;
@@ -243,11 +254,11 @@ __device__ __forceinline__ LpSum lp_join(LpSum t, float scale2) {
   for (int i = 0; i < W; i++) o[i] = part[min(i, waves - 1)];
 #pragma unroll
   for (int i = 0; i < W; i++) m = fmaxf(m, o[i][0]);
-  LpSum r = {m, 0.0f, 0.0f};
+  LpSum r = {m, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < W; i++) {
-    LpSum w = {o[i][0], o[i][1], o[i][2]};
-    lp_shift(w, m, scale2);
+    LpSum w = {o[i][0], o[i][1], o[i][2], 0.0f, 0.0f};
+    lp_shift(w, m, scale2, false);
     r.s += i < waves ? w.s : 0.0f;
     r.w += i < waves ? w.w : 0.0f;
   }
@@ -258,19 +269,28 @@ __device__ __forceinline__ LpSum lp_join(LpSum t, float scale2) {
 template <int XT> struct LpRaw { u32x4 v[XT == LP_F16 || XT == LP_BF16 ? 1 : 2]; floatx4 cs[XT == LP_I32 ? 2 : 1]; };
 template <int XT> constexpr int LP_SIZE = XT == LP_F16 || XT == LP_BF16 ? 2 : 4;
 
-// A whole piece of LP_V columns from column c on; where it is not whole, the row's first one, not used.
-template <int XT>
+// A whole piece of LP_V columns from column c on; where it is not whole, the row's first one, not used. STREAM: past
+// the caches' reuse.
+template <int XT, bool STREAM>
 __device__ __forceinline__ void lp_load(LpRaw<XT>& r, const uint8_t* row, const float* col_scale, int64_t c, bool whole,
                                         int64_t cols) {
   if (cols < LP_V) return;
   const int64_t at = whole ? c : 0;
   const u32x4* p = (const u32x4*)(row + at * LP_SIZE<XT>);
-  r.v[0] = p[0];
-  if constexpr (LP_SIZE<XT> == 4) r.v[1] = p[1];
+#pragma unroll
+  for (int i = 0; i < LP_SIZE<XT> / 2; i++) {
+    if constexpr (STREAM) r.v[i] = __builtin_nontemporal_load(p + i);
+    else r.v[i] = p[i];
+  }
   if constexpr (XT == LP_I32) {
     r.cs[0] = *(const floatx4*)(col_scale + at);
     r.cs[1] = *(const floatx4*)(col_scale + at + 4);
   }
+}
+
+template <bool STREAM, typename V> __device__ __forceinline__ void lp_store(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
 }
 
 template <int XT>
@@ -313,7 +333,7 @@ __device__ __forceinline__ void lp_write(const LpArgs& A, int64_t row, const LpS
     A.stats[2 * row] = t.s == t.s ? t.m : NAN;
     A.stats[2 * row + 1] = none ? INFINITY : logs;
   }
-  if (A.entropy) A.entropy[row] = none ? 0.0f : logs - A.scale * (t.w / t.s);
+  if (A.entropy) A.entropy[row] = none ? 0.0f : logs - 0.693147180559945f * (t.w / t.s);
   if (A.logprob) {
     float lp = none ? -INFINITY : (given - t.m) * A.scale - logs;
     if (token < 0) lp = 0.0f;
@@ -420,7 +440,7 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
 }
 
 // One block a slice of a row, LP_U pieces a thread at a time and the next ones on their way.
-template <int XT, bool ENT, bool TOP>
+template <int XT, bool ENT, bool TOP, bool STREAM>
 __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (block >= A.rows * A.slices) return;
@@ -433,7 +453,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
   int64_t token = -1;
   const float given = A.slices == 1 ? lp_given<XT>(A, row, token) : 0.0f;
 
-  LpSum t = {-FLT_MAX, 0.0f, 0.0f};
+  LpSum t = {-FLT_MAX, 0.0f, 0.0f, -FLT_MAX, 0.0f};
   auto take = [&](const LpRaw<XT> (&raw)[LP_U], int b) {
     float x[LP_U][LP_V], most = -INFINITY;
 #pragma unroll
@@ -450,17 +470,22 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
 #pragma unroll
       for (int i = 0; i < LP_V; i += 2) most = lp_max3(most, x[u][i], x[u][i + 1]);
     }
-    if (most > t.m) lp_shift(t, most, A.scale2);
+    if (most > t.m) lp_shift(t, most, A.scale2, true);
+    const bool near = lp_near(t.ms);
 #pragma unroll
     for (int u = 0; u < LP_U; u++) {
       if (u > 0 && b + u * (int)blockDim.x >= end) break;
       float s = 0.0f;
+      auto sums = [&](auto exponent) {
 #pragma unroll
-      for (int i = 0; i < LP_V; i++) {
-        const float d = x[u][i] - t.m, e = __builtin_amdgcn_exp2f(d * A.scale2);
-        s += e;
-        if constexpr (ENT) t.w = __builtin_fmaf(e, fmaxf(d, -FLT_MAX), t.w);   // e is 0 where d is infinite
-      }
+        for (int i = 0; i < LP_V; i++) {
+          const float d = exponent(x[u][i]), e = __builtin_amdgcn_exp2f(d);
+          s += e;
+          if constexpr (ENT) t.w = __builtin_fmaf(e, fmaxf(d, -200.0f), t.w);   // e is 0 below that, infinite d among them
+        }
+      };
+      if (near) sums([&](float v) { return __builtin_fmaf(v, A.scale2, -t.ms); });
+      else sums([&](float v) { return (v - t.m) * A.scale2; });
       t.s += s;
     }
   };
@@ -468,18 +493,20 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
 #pragma unroll
     for (int u = 0; u < LP_U; u++) {
       const int at = b + u * (int)blockDim.x + (int)threadIdx.x;
-      lp_load<XT>(raw[u], xr, A.col_scale, (int64_t)at * LP_V, at < full, A.cols);
+      lp_load<XT, STREAM>(raw[u], xr, A.col_scale, (int64_t)at * LP_V, at < full, A.cols);
     }
   };
 
   LpRaw<XT> raw[LP_U], next[LP_U];
   const int step = LP_U * (int)blockDim.x;
   load(raw, begin);
-  for (int b = begin; b < end; b += step) {
+#pragma unroll 1
+  for (int b = begin; b < end; b += 2 * step) {
     if (b + step < end) load(next, b + step);
     take(raw, b);
-#pragma unroll
-    for (int u = 0; u < LP_U; u++) raw[u] = next[u];
+    if (b + step >= end) break;
+    if (b + 2 * step < end) load(raw, b + 2 * step);
+    take(next, b + step);
   }
 
   // -FLT_MAX stands for nothing but -infinity; a row's lowest logit may be it, and then
@@ -523,10 +550,10 @@ __global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
   if (row >= A.rows) return;
   int64_t token;
   const float given = lp_given<XT>(A, row, token);
-  LpSum t = {-FLT_MAX, 0.0f, 0.0f};
+  LpSum t = {-FLT_MAX, 0.0f, 0.0f, -FLT_MAX, 0.0f};
   if ((int)threadIdx.x < A.slices) {
     const floatx4 v = A.part[row * A.slices + threadIdx.x];
-    t = LpSum{v[0], v[1], v[2]};
+    t = LpSum{v[0], v[1], v[2], -FLT_MAX, 0.0f};
   }
   if constexpr (TOP) {
     __shared__ LpLists<LP_JOIN / 64> lds;
@@ -551,8 +578,8 @@ __global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
 
 // dx_i = scale (g [i = t] - p_i (g + h (log p_i + H))), g and h the gradients of the
 // row's log probability and entropy H; p_i from the forward's largest and sum. Below
-// e^-200 p is 0 in fp32, and the log is held there for infinite ones.
-template <int XT, bool ENT>
+// 2^-300 p is 0 in fp32, and the log is held there for infinite ones.
+template <int XT, bool ENT, bool STREAM>
 __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
   constexpr int U = 4;
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -564,7 +591,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = (first + u * LP_THREADS) * LP_V;
-    lp_load<XT>(raw[u], xr, nullptr, c, c + LP_V <= A.cols, A.cols);
+    lp_load<XT, STREAM>(raw[u], xr, nullptr, c, c + LP_V <= A.cols, A.cols);
   }
   const int64_t token = A.tokens ? A.tokens[row] : -1;
   const float m = A.stats[2 * row], logs = A.stats[2 * row + 1];
@@ -573,6 +600,8 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
   if (logs == INFINITY) g = 0.0f;                 // no weight in the row
   float h = 0.0f, H = 0.0f;
   if constexpr (ENT) { h = A.g_entropy[row]; H = A.entropy[row]; }
+  const float own = A.scale * g, g2 = -A.scale * __builtin_fmaf(h, H, g), h2 = -A.scale * h * 0.693147180559945f;
+  const float logs2 = logs * 1.44269504088896f;
 #pragma unroll
   for (int u = 0; u < U; u++) {
     const int64_t c = (first + u * LP_THREADS) * LP_V;
@@ -585,21 +614,21 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
 #pragma unroll
       for (int i = 0; i < LP_V; i++) x[i] = c + i < A.cols ? lp_one<XT>(xr, nullptr, 1.0f, c + i) : 0.0f;
     }
+    // with the token's own term where it is: - scale (g + h (log p + H)) p, its logs in base 2
 #pragma unroll
     for (int i = 0; i < LP_V; i++) {
-      const float lp = __builtin_fmaf(x[i] - m, A.scale, -logs);
-      const float p = __builtin_amdgcn_exp2f(lp * 1.44269504088896f);
-      float k = g;
-      if constexpr (ENT) k = __builtin_fmaf(h, fmaxf(lp, -200.0f) + H, g);
-      x[i] = p * k;
+      const float lp = __builtin_fmaf(x[i] - m, A.scale2, -logs2), p = __builtin_amdgcn_exp2f(lp);
+      x[i] = p * (ENT ? __builtin_fmaf(h2, fmaxf(lp, -300.0f), g2) : g2);
     }
     const uint64_t at = (uint64_t)(token - c);
+    if (at < LP_V) {
 #pragma unroll
-    for (int i = 0; i < LP_V; i++) x[i] = A.scale * ((at == (uint64_t)i ? g : 0.0f) - x[i]);
+      for (int i = 0; i < LP_V; i++) x[i] += at == (uint64_t)i ? own : 0.0f;
+    }
     if constexpr (LP_SIZE<XT> == 4) {
       if (whole) {
-        ((floatx4*)(dr + c * 4))[0] = floatx4{x[0], x[1], x[2], x[3]};
-        ((floatx4*)(dr + c * 4))[1] = floatx4{x[4], x[5], x[6], x[7]};
+        lp_store<STREAM>((floatx4*)(dr + c * 4), floatx4{x[0], x[1], x[2], x[3]});
+        lp_store<STREAM>((floatx4*)(dr + c * 4) + 1, floatx4{x[4], x[5], x[6], x[7]});
       } else {
 #pragma unroll
         for (int i = 0; i < LP_V; i++)
@@ -613,7 +642,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
         u32x4 w;
 #pragma unroll
         for (int i = 0; i < 4; i++) w[i] = (uint32_t)o[2 * i] | (uint32_t)o[2 * i + 1] << 16;
-        *(u32x4*)(dr + c * 2) = w;
+        lp_store<STREAM>((u32x4*)(dr + c * 2), w);
       } else {
 #pragma unroll
         for (int i = 0; i < LP_V; i++)
@@ -629,9 +658,14 @@ static dim3 lp_grid(int64_t blocks) {
   return dim3((unsigned)across, (unsigned)((blocks + across - 1) / across));
 }
 
+// Logits that the caches do not hold until they are read again (256 MB on this card) are read past them.
+static bool lp_streams(int64_t rows, int64_t cols, int size) { return rows * cols * size >= (int64_t)1 << 29; }
+
 template <int XT, bool ENT, bool TOP>
 hipError_t lp_go(const LpArgs& a, int threads, hipStream_t s) {
-  hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP>), lp_grid(a.rows * a.slices), dim3((unsigned)threads), 0, s, a);
+  const dim3 grid = lp_grid(a.rows * a.slices);
+  if (lp_streams(a.rows, a.cols, LP_SIZE<XT>)) hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP, true>), grid, dim3((unsigned)threads), 0, s, a);
+  else hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP, false>), grid, dim3((unsigned)threads), 0, s, a);
   if (a.slices > 1) hipLaunchKernelGGL((lp_join_kernel<XT, TOP>), lp_grid(a.rows), dim3(TOP ? LP_JOIN : 64), 0, s, a);
   return hipGetLastError();
 }
@@ -645,8 +679,13 @@ hipError_t lp_types(const LpArgs& a, int threads, hipStream_t s) {
 template <int XT>
 hipError_t lp_back(const LpBackArgs& a, hipStream_t s) {
   const dim3 grid = lp_grid(a.rows * a.parts), threads(LP_THREADS);
-  if (a.g_entropy) hipLaunchKernelGGL((lp_backward_kernel<XT, true>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((lp_backward_kernel<XT, false>), grid, threads, 0, s, a);
+  if (lp_streams(a.rows, a.cols, LP_SIZE<XT>)) {
+    if (a.g_entropy) hipLaunchKernelGGL((lp_backward_kernel<XT, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((lp_backward_kernel<XT, false, true>), grid, threads, 0, s, a);
+  } else {
+    if (a.g_entropy) hipLaunchKernelGGL((lp_backward_kernel<XT, true, false>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((lp_backward_kernel<XT, false, false>), grid, threads, 0, s, a);
+  }
   return hipGetLastError();
 }
 
@@ -782,6 +821,7 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
   a.ldg = p.ldg;
   a.parts = (int)((p.cols + 4 * LP_THREADS * LP_V - 1) / (4 * LP_THREADS * LP_V));
   a.scale = p.scale;
+  a.scale2 = (float)((double)p.scale * 1.4426950408889634);
   hipStream_t s = (hipStream_t)stream;
   switch (p.type_x) {
     case NM_F16: return layer_hip(lp_back<LP_F16>(a, s));

@@ -358,3 +358,26 @@ def test_wrapper_refuses():
             token_logprobs(*args, **kw)
     with pytest.raises(RuntimeError, match="gradient"):
         token_logprobs(Rows(x.int(), scales[0].clone().requires_grad_(), scales[1]), at)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_past_the_caches_give_the_same(dtype):
+    """512 MB and more are read past the caches: a row's results do not depend on that."""
+    rows, cols = (2048, 131072) if dtype == "bf16" else (1100, 131000)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (2 * torch.randn((rows, cols), generator=g, device="cuda")).to(TORCH[dtype])
+    tokens = torch.randint(0, cols, (rows,), generator=g, device="cuda")
+    gl, ge = torch.randn(rows, generator=g, device="cuda"), torch.randn(rows, generator=g, device="cuda")
+    got = []
+    for n in (rows, 1030):
+        plan = nm.nm_logprobs_plan_init(n, cols, dtype=dtype, top=7)
+        assert plan.workspace_bytes == 0
+        out = [torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty((n, 2), device="cuda"),
+               torch.empty((n, 7), device="cuda"), torch.empty((n, 7), dtype=torch.int64, device="cuda"), torch.empty_like(x[:n])]
+        nm.nm_logprobs(plan, x[:n], tokens[:n], out[0], entropy=out[1], stats=out[2], top_logprob=out[3], top_index=out[4])
+        nm.nm_logprobs_backward(plan, x[:n], tokens[:n], out[2], out[5], g_logprob=gl[:n], g_entropy=ge[:n], entropy=out[1])
+        got.append(out)
+    for a, b in zip(*got):
+        assert torch.equal(a[:1030], b)
+    logp = torch.log_softmax(x[-3:].double(), 1)
+    close(got[0][0][-3:], logp.gather(1, tokens[-3:, None])[:, 0].cpu(), torch.full((3,), 1e-4, dtype=torch.float64), "logprob")
