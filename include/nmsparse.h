@@ -519,7 +519,8 @@ nm_status_t nm_lora_workspace_size(nm_lora_plan_t plan, size_t* bytes);
 
 /* d_x_scale (n floats) is given exactly where x is NM_I8, d_row_scale (n) and
  * d_col_scale (m) exactly where base is NM_I32. d_scale: adapters floats. d_workspace:
- * nm_lora_workspace_size bytes; scratch, as for nm_spmm. */
+ * nm_lora_workspace_size bytes; scratch, as for nm_spmm. A token's y does not depend on
+ * the other tokens of its call. */
 nm_status_t nm_lora(nm_lora_plan_t plan, const void* dX, const float* d_x_scale, const void* dA, const void* dB,
                     const float* d_scale, const int64_t* d_index, const void* d_base, const float* d_row_scale,
                     const float* d_col_scale, void* dY, void* d_workspace, void* stream);

@@ -17,6 +17,7 @@ struct nm_lora_plan {
   int tiles;              // of 64 tokens
   int splits, loops;      // parts of k; a wave takes LORA_KW k that many times
   int slots_in, slots_out; // blocks that share out a tile's adapters
+  bool sorted;            // the tokens are sorted by their adapters first
 };
 
 namespace nm {
@@ -24,8 +25,12 @@ namespace nm {
 constexpr int LORA_TILE = 64;      // tokens that are sorted into adapters together: a wave's lanes
 constexpr int LORA_WAVES = 8;      // waves a block
 constexpr int LORA_KW = 128;       // k that a wave takes at a time
+constexpr int LORA_SORT_THREADS = 1024;
+constexpr int LORA_SORT_BINS = 4096;
 constexpr int LORA_FEATURES = 256; // outputs a block of the outer product, or twice as many
 constexpr int64_t LORA_MANY = 1 << 17; // outputs of all groups that are more than the CUs take at a time
+
+typedef int intx2 __attribute__((ext_vector_type(2)));
 
 struct LoraArgs {
   const uint8_t* x;
@@ -39,6 +44,7 @@ struct LoraArgs {
   const float* col_scale;
   uint16_t* y;
   float* t;               // splits x n x rank
+  const intx2* order;     // (name, token) sorted by names, or NULL: the tokens as they come
   int64_t m, n, k, ldx, lda, ldc, ldy;
   int adapters, rank, splits, loops;
   bool in_place;          // base is y: rows without an adapter stay
@@ -62,13 +68,91 @@ __device__ __forceinline__ void lora_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
 }
 
-// The adapters of a tile's tokens, one lane a token: its adapter, -1 for none, -2 for one
-// that does not exist, -3 behind the last token.
-__device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0) {
+// An index as the kernels take it: its adapter, -1 for none, -2 for one that does not exist.
+__device__ __forceinline__ int lora_name(const LoraArgs& A, int64_t i) { return i < 0 ? -1 : i < A.adapters ? (int)i : -2; }
+
+// A tile's tokens, one a lane, and their names (-3 behind the last token): in their own order, or in that of
+// lora_sort_kernel.
+__device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0, int& token) {
   const int64_t at = tile0 + (threadIdx.x & 63);
+  token = (int)at;
   if (at >= A.n) return -3;
-  const int64_t i = A.index[at];
-  return i < 0 ? -1 : i < A.adapters ? (int)i : -2;
+  if (A.order) {
+    const intx2 o = A.order[at];
+    token = o[1];
+    return o[0];
+  }
+  return lora_name(A, A.index[at]);
+}
+
+// Tokens by their adapters, so that a tile holds few of them: a count of each bin of names, the
+// counts' sums, and the tokens put behind them. Adapters 4096 apart share a bin, and a tile holds
+// whatever it gets: the order is for speed alone. One block; the order within a bin is that in
+// which the atomics are served, and no token's result depends on it: each is a column of its own.
+// It takes 4 us with its launch, at 65 tokens as at 4096 (latency: the index, places, sums, the
+// order), which a prompt in runs pays for nothing: 4096 tokens, 64 adapters of rank 16, k = m =
+// 4096, bf16, in runs 26.0 us without it and 29.7 with it, scattered 207 and 37.3. So it runs from
+// where scattered tokens gain about that: 256 tokens over 64 adapters 34.7 us without and 27.5
+// with, over 8 14.6 and 16.3; 1024 over 8 29.8 and 23.5, over 4 23.1 and 23.4; 4096 over 4 40.8
+// and 30.7, over 2 30.9 and 30.8; 128 over 64 16.1 and 18.5.
+__global__ void __launch_bounds__(LORA_SORT_THREADS) lora_sort_kernel(LoraArgs A, intx2* order) {
+  constexpr int T = LORA_SORT_THREADS, B = LORA_SORT_BINS / T, U = 4;
+  __shared__ int bins[LORA_SORT_BINS];
+  __shared__ int taken;
+  const int lane = threadIdx.x & 63;
+  int name[U], nth[U];
+  auto load = [&](int64_t b) {
+    int64_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) v[u] = A.index[min(b + u * T + threadIdx.x, A.n - 1)];
+#pragma unroll
+    for (int u = 0; u < U; u++) name[u] = b + u * T + threadIdx.x < A.n ? lora_name(A, v[u]) + 2 : -1;
+  };
+  auto bin = [](int of) { return of & (LORA_SORT_BINS - 1); };
+  // Each token's place in its bin. A wave whose tokens are of one name takes its places at
+  // once, by lane 0 (behind the last token there are only last lanes); other lanes add 0.
+  auto place = [&] {
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const uint64_t here = __ballot(name[u] >= 0);
+      const int lead = __builtin_amdgcn_readfirstlane(name[u]);
+      const bool one = here && __ballot(name[u] == lead) == here;
+      const int add = one ? (lane == 0 ? __popcll(here) : 0) : name[u] >= 0;
+      nth[u] = atomicAdd(&bins[add ? bin(name[u]) : lane], add);
+      if (one) nth[u] = __builtin_amdgcn_readfirstlane(nth[u]) + lane;
+    }
+  };
+  load(0);
+#pragma unroll
+  for (int i = 0; i < B; i++) bins[threadIdx.x + i * T] = 0;
+  if (threadIdx.x == 0) taken = 0;
+  __syncthreads();
+  place();
+  for (int64_t b = U * T; b < A.n; b += U * T) {
+    load(b);
+    place();
+  }
+  __syncthreads();
+  // the bins' first places, in whatever order the threads come
+#pragma unroll
+  for (int i = 0; i < B; i++) {
+    const int tokens = bins[threadIdx.x + i * T];
+    if (tokens) bins[threadIdx.x + i * T] = atomicAdd(&taken, tokens);
+  }
+  __syncthreads();
+  if (A.n <= U * T) {
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (name[u] >= 0) order[bins[bin(name[u])] + nth[u]] = intx2{name[u] - 2, (int)(u * T + threadIdx.x)};
+    return;
+  }
+  for (int64_t b = 0; b < A.n; b += U * T) {
+    load(b);
+    place();
+#pragma unroll
+    for (int u = 0; u < U; u++)
+      if (name[u] >= 0) order[nth[u]] = intx2{name[u] - 2, (int)(b + u * T + threadIdx.x)};
+  }
 }
 
 // The groups of a tile (the tokens of one adapter, or of none) that fall to one of gridDim.z
@@ -135,7 +219,8 @@ template <bool OWN> struct LoraColumns {
   uint64_t group;
   int count;              // columns that may hold one
 
-  __device__ __forceinline__ void set(int* l, uint64_t g) {
+  // mine: the lane's token
+  __device__ __forceinline__ void set(int* l, uint64_t g, int mine) {
     list = l;
     group = g;
     count = OWN ? 16 : __popcll(g);
@@ -143,11 +228,12 @@ template <bool OWN> struct LoraColumns {
       const int lane = threadIdx.x & 63;
       lora_lds_order();
       if (g >> lane & 1)
-        list[__builtin_amdgcn_mbcnt_hi((uint32_t)(g >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)g, 0))] = lane;
+        list[__builtin_amdgcn_mbcnt_hi((uint32_t)(g >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)g, 0))] = mine;
       lora_lds_order();
     }
   }
-  // whether a column holds one of the group's tokens, and its token (another of the group where it does not)
+  // whether a column holds one of the group's tokens, and its token (another of the group where it does not;
+  // up to 16 tokens are one tile in their own order)
   __device__ __forceinline__ bool has(int col) const { return OWN ? group >> col & 1 : col < count; }
   __device__ __forceinline__ int token(int col) const {
     return OWN ? (has(col) ? col : __builtin_ctzll(group)) : list[min(col, count - 1)];
@@ -169,7 +255,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
   __shared__ int tokens[OWN ? 1 : LORA_WAVES][LORA_TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
   const int64_t tile0 = (int64_t)blockIdx.y * LORA_TILE;
-  const int mine = lora_named(A, tile0);
+  int at_lane;
+  const int mine = lora_named(A, tile0, at_lane);
   const int rank_tiles = (A.rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
   const int rt = wave % across, part = wave / across, parts = LORA_WAVES / across;
 
@@ -179,7 +266,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
   int adapter;
   while (groups.next(group, adapter)) {
     cols_t cols;
-    cols.set(tokens[OWN ? 0 : wave], group);
+    cols.set(tokens[OWN ? 0 : wave], group, at_lane);
     const uint8_t* const ar = (const uint8_t*)(A.a + ((int64_t)adapter * A.rank + min(16 * rt + l16, A.rank - 1)) * A.lda);
     for (int c0 = 0; c0 < cols.count; c0 += 16 * NT) {
       floatx4 acc[NT];
@@ -189,7 +276,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
       auto product = [&](auto J) {
         const uint8_t* xr[J.n];
 #pragma unroll
-        for (int j = 0; j < J.n; j++) xr[j] = A.x + (tile0 + cols.token(c0 + 16 * j + l16)) * A.ldx * (X8 ? 1 : 2);
+        for (int j = 0; j < J.n; j++) xr[j] = A.x + (int64_t)cols.token(c0 + 16 * j + l16) * A.ldx * (X8 ? 1 : 2);
         constexpr int JN = decltype(J)::n;
         typedef LoraStep<JN, XS> step_t;
         auto first_k = [&](int i) { return (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW; };
@@ -264,7 +351,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
         floatx4 v = red[r][j][lane];
         for (int w = 1; w < parts; w++) v += red[r + w * across][j][lane];
         if (cols.has(col) && rank < A.rank)
-          *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + tile0 + cols.token(col)) * A.rank + rank) = v;
+          *(floatx4*)(A.t + ((int64_t)blockIdx.x * A.n + cols.token(col)) * A.rank + rank) = v;
       }
       __syncthreads();
     }
@@ -299,7 +386,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
   int64_t out[FB];
 #pragma unroll
   for (int b = 0; b < FB; b++) out[b] = first_out(b, q);
-  const int mine = lora_named(A, tile0);
+  int at_lane;
+  const int mine = lora_named(A, tile0, at_lane);
   const int chunks = A.rank / 8;
 
   floatx4 cs[FB][2];
@@ -317,12 +405,12 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
   while (groups.next(group, adapter)) {
     if (adapter == -1 && A.in_place) continue;
     cols_t cols;
-    cols.set(tokens[OWN ? 0 : wave], group);
+    cols.set(tokens[OWN ? 0 : wave], group, at_lane);
     const float sa = adapter >= 0 ? A.scale[adapter] : adapter == -1 ? 0.0f : __builtin_nanf("");
     for (int c0 = 0; c0 < cols.count; c0 += 16 * NT) {
       // t first: what is behind it is not waited for until it is in LDS
       auto part = [&](int e, int s) {
-        const float* p = A.t + (tile0 + cols.token(c0 + e / PER)) * A.rank + min(e % PER * 4, A.rank - 4);
+        const float* p = A.t + (int64_t)cols.token(c0 + e / PER) * A.rank + min(e % PER * 4, A.rank - 4);
         return *(const floatx4*)(p + (int64_t)min(s, A.splits - 1) * A.n * A.rank);
       };
       floatx4 w[WS];
@@ -353,8 +441,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
       for (int j = 0; j < NT; j++) {
         in[j] = cols.has(c0 + 16 * j + l16);
         token[j] = cols.token(c0 + 16 * j + l16);
-        rs[j] = ACC ? A.row_scale[tile0 + token[j]] : 1.0f;
-        const uint8_t* const p = A.base + (tile0 + token[j]) * A.ldc * (ACC ? 4 : 2);
+        rs[j] = ACC ? A.row_scale[token[j]] : 1.0f;
+        const uint8_t* const p = A.base + (int64_t)token[j] * A.ldc * (ACC ? 4 : 2);
 #pragma unroll
         for (int b = 0; b < FB; b++)
 #pragma unroll
@@ -364,7 +452,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
 #pragma unroll 1
         for (int e = threadIdx.x; e < 16 * NT * PER; e += THREADS) {
           const int j = e / PER, r = e % PER * 4;
-          if (A.x_scale) xs = A.x_scale[tile0 + cols.token(c0 + j)];
+          if (A.x_scale) xs = A.x_scale[cols.token(c0 + j)];
           floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int s = 0; s < A.splits; s += WS) {          // the parts of k in their order
             if (e >= THREADS || s > 0) {
@@ -407,7 +495,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
 #pragma unroll
       for (int j = 0; j < NT; j++) {
         if (c0 + 16 * j >= cols.count) break;
-        const int64_t at = tile0 + token[j];
+        const int64_t at = token[j];
         const uint16_t* const tj = ts[16 * j + l16];
         const float fac = factor[16 * j + l16];
 #pragma unroll
@@ -493,6 +581,7 @@ hipError_t lora_outer(const LoraArgs& a, const nm_lora_plan& pl, hipStream_t s) 
 template <int IO>
 hipError_t lora_go(const LoraArgs& a, const nm_lora_plan& pl, hipStream_t s) {
   const bool acc = pl.p.type_base == NM_I32;
+  if (a.order) hipLaunchKernelGGL(lora_sort_kernel, dim3(1), dim3(LORA_SORT_THREADS), 0, s, a, (intx2*)a.order);
   hipError_t e = pl.p.type_x == NM_I8 ? lora_inner<IO, true>(a, pl, s) : lora_inner<IO, false>(a, pl, s);
   if (e != hipSuccess) return e;
   const int r = a.rank;
@@ -547,6 +636,7 @@ nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* p) 
   pl->splits = (int)((steps + pl->loops - 1) / pl->loops);
   pl->slots_in = slots(tiles * pl->splits);
   pl->slots_out = slots(tiles * ((p->m + LORA_FEATURES - 1) / LORA_FEATURES + 1));
+  pl->sorted = p->n >= 256 && p->adapters >= 4 && p->n * p->adapters >= 8192;  // figures at lora_sort_kernel
   *plan = pl;
   return layer_fail(NM_OK, "");
 }
@@ -559,7 +649,7 @@ nm_status_t nm_lora_plan_destroy(nm_lora_plan_t plan) {
 nm_status_t nm_lora_workspace_size(nm_lora_plan_t plan, size_t* bytes) {
   if (!plan || !bytes) return layer_fail(NM_ERR_INVALID_ARG, "plan / bytes is NULL");
   const nm_lora_problem_t& p = plan->p;
-  *bytes = (size_t)plan->splits * p.n * p.rank * sizeof(float);
+  *bytes = (size_t)plan->splits * p.n * p.rank * sizeof(float) + (plan->sorted ? (size_t)p.n * 8 : 0);
   return NM_OK;
 }
 
@@ -593,6 +683,7 @@ nm_status_t nm_lora(nm_lora_plan_t plan, const void* dX, const float* d_x_scale,
   a.col_scale = d_col_scale;
   a.y = (uint16_t*)dY;
   a.t = (float*)d_workspace;
+  if (plan->sorted) a.order = (const intx2*)(a.t + (size_t)plan->splits * p.n * p.rank);
   a.m = p.m;
   a.n = p.n;
   a.k = p.k;

@@ -169,15 +169,35 @@ def test_f16_inner_products_beyond_f16(x, k, up):
     check(s, 16)
 
 
-def test_a_token_does_not_depend_on_the_others():
-    s = inputs(150, 700, 300, 32, 5, "bf16")
+@pytest.mark.parametrize("n,k,m,r,count,mix", [
+    (256, 130, 65, 8, 32, "scattered"), (300, 300, 130, 16, 64, "scattered"), (2048, 64, 40, 40, 4, "scattered"),
+    (2047, 100, 72, 16, 5, "runs"), (4096, 32, 33, 8, 9, "scattered"), (4097, 32, 33, 24, 9, "scattered"), (9000, 48, 24, 8, 200, "runs"),
+    (700, 16, 8, 8, 9000, "scattered")])
+@pytest.mark.parametrize("dtype,x,base", [("f16", "i8", "i32"), ("bf16", "16", "16")])
+def test_tokens_sorted_by_their_adapters(n, k, m, r, count, mix, dtype, x, base):
+    s = inputs(n, k, m, r, count, dtype, x, base, seed=n, mix=mix)
+    if count == 9000:                     # adapters that share a bin of the sort
+        s["index"] = torch.where(s["index"] < 0, s["index"], s["index"] % 3 * 4096 + 5)
+        s["index"][s["index"] >= count] = 4101
+    y = check(s, r)
+    assert torch.equal(run(s, r), y)
+    named, far = s["index"].clone(), torch.arange(n) % 11 == 3
+    named[far] = count + torch.arange(int(far.sum())) * (1 << 40)
+    named[~far & (s["index"] < 0)] = -(1 << 50)
+    z = run(s, r, index=named)
+    assert z[far.cuda()].isnan().all() and torch.equal(z[~far.cuda()], y[~far.cuda()])
+
+
+@pytest.mark.parametrize("n", [150, 1700])
+def test_a_token_does_not_depend_on_the_others(n):
+    s = inputs(n, 700, 300, 32, 5, "bf16")
     y = run(s, 32)
-    order = torch.randperm(150, generator=gen(3))
+    order = torch.randperm(n, generator=gen(3))
     for name in ("x", "index", "base"):
         s[name] = s[name][order]
     assert torch.equal(run(s, 32), y[order.cuda()])
-    s["index"][75:] = -1                  # the others' adapters leave
-    assert torch.equal(run(s, 32)[:75], y[order.cuda()][:75])
+    s["index"][n // 2:] = -1              # the others' adapters leave
+    assert torch.equal(run(s, 32)[:n // 2], y[order.cuda()][:n // 2])
 
 
 def test_nothing_to_do():

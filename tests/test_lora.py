@@ -41,6 +41,9 @@ def test_workspace(n, k, r):
     b = plan(n=n, k=k, rank=r, ldx=(k + 7) // 8 * 8, lda=(k + 7) // 8 * 8).workspace_bytes
     assert b % (n * r * 4) == 0 and 1 <= b // (n * r * 4) <= 16
     assert plan(n=0).workspace_bytes == 0
+    if n >= 4096:                         # tokens over 4 adapters and more are sorted by them: 8 bytes each
+        more = plan(n=n, k=k, rank=r, ldx=(k + 7) // 8 * 8, lda=(k + 7) // 8 * 8, adapters=4).workspace_bytes
+        assert more == b + 8 * n
     assert nm.lib().nm_lora_workspace_size(None, None) == nm.NM_ERR_INVALID_ARG
 
 
