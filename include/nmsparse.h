@@ -402,7 +402,8 @@ nm_status_t nm_w4_matvec(nm_w4_plan_t plan, const void* d_packed, const void* dX
  * Everything is computed in fp32 and rounded once to type_io; a head's sum of
  * squares has fp32's range, as a row's has in nm_rmsnorm, and a head of zeros with
  * eps = 0 is NaN. A row whose position is negative holds no token: its y stays as it
- * was. A position of table_rows or more has no angles: the turned elements are NaN. */
+ * was, or becomes zeros (zero_rows). A position of table_rows or more has no angles:
+ * the turned elements are NaN. */
 typedef enum { NM_PAIRS_HALVES = 0, NM_PAIRS_NEIGHBOURS = 1 } nm_pairs_t;
 typedef struct {
   int64_t rows;             /* tokens, < 2^24 */
@@ -415,6 +416,7 @@ typedef struct {
   int64_t table_rows;       /* positions that the table holds, up to 2^31 */
   int64_t ldx, ldy;         /* rows of x (and its gradient), of y (and its gradient) */
   float eps;                /* finite and >= 0 */
+  int32_t zero_rows;        /* rows of y that hold no token: 0, left as they were; 1, zeros */
 } nm_heads_problem_t;
 typedef struct nm_heads_plan* nm_heads_plan_t;
 nm_status_t nm_heads_plan_init(nm_heads_plan_t* plan, const nm_heads_problem_t* problem);

@@ -60,7 +60,8 @@ class nm_heads_problem_t(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
                 ("heads_v", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
                 ("pairs", ctypes.c_int32), ("type_io", ctypes.c_int32), ("type_x", ctypes.c_int32),
-                ("table_rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_float)]
+                ("table_rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("zero_rows", ctypes.c_int32)]
 
 
 class nm_logprobs_problem_t(ctypes.Structure):
@@ -632,16 +633,17 @@ class HeadsPlan(_LayerPlan):
 
 
 def nm_heads_plan_init(rows, heads_q, heads_k, heads_v, head_dim, rotary_dim, pairs="halves", table_rows=0, dtype="f16",
-                       x_dtype=None, ldx=None, ldy=None, eps=1e-6):
+                       x_dtype=None, ldx=None, ldy=None, eps=1e-6, zero_rows=False):
     """Plan of the norms of query and key heads with their rotation (host only). pairs: "halves" (i, i + rotary_dim / 2)
     or "neighbours" (2i, 2i + 1); table_rows: the positions that the table of angles holds; dtype: the 16-bit type of y
-    and the gains; x_dtype: dtype, or "i32" for an int8 product's accumulators."""
+    and the gains; x_dtype: dtype, or "i32" for an int8 product's accumulators; zero_rows: rows of y that hold no token
+    become zeros (else they stay as they were)."""
     if pairs not in PAIRS:
         raise ValueError("pairs must be one of %s, got %r" % (sorted(PAIRS), pairs))
     x_dtype = x_dtype or dtype
     p = nm_heads_problem_t()
     p.rows, p.heads_q, p.heads_k, p.heads_v, p.head_dim, p.rotary_dim = rows, heads_q, heads_k, heads_v, head_dim, rotary_dim
-    p.pairs, p.table_rows, p.eps = PAIRS[pairs], table_rows, eps
+    p.pairs, p.table_rows, p.eps, p.zero_rows = PAIRS[pairs], table_rows, eps, bool(zero_rows)
     p.type_io, p.type_x = _dtype_code(dtype), _dtype_code(x_dtype)
     cols = max(1, (heads_q + heads_k + heads_v) * head_dim)
     p.ldx = ldx if ldx is not None else cols

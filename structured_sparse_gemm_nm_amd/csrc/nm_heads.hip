@@ -30,7 +30,7 @@ struct HeadArgs {
   uint16_t* y;          // backward: dx
   float* part;          // backward: the blocks' shares of the gains' gradients, 2 x dim each
   int64_t rows, table_rows, ldx, ldy, lddy;
-  int q, normed, heads, dim, rotary;
+  int q, normed, heads, dim, rotary, zero_rows;
   float eps, rdim;      // rdim = 1 / dim
 };
 
@@ -145,13 +145,20 @@ template <int IO, bool ACC, bool HALVES, int G>
 __global__ void __launch_bounds__(HEAD_THREADS) heads_kernel(HeadArgs A) {
   const int64_t token = blockIdx.x;
   const int64_t pos = A.positions[token];
-  if (pos < 0) return;                            // no token: its row stays as it was
+  if (pos < 0 && !A.zero_rows) return;            // no token: its row stays as it was
   const int j = threadIdx.x % G;
   const int first = blockIdx.y * (HEAD_THREADS / G) + threadIdx.x / G, step = gridDim.y * (HEAD_THREADS / G);
   HeadLane<HALVES> l;
   l.place(A, j);
   const uint8_t* const row = A.x + token * A.ldx * (ACC ? 4 : 2);
   uint16_t* const out = A.y + token * A.ldy;
+  if (pos < 0) {
+    for (int h = first; h < A.heads && l.in; h += step) {
+      uint16_t* const to = out + (int64_t)h * A.dim;
+      *(u32x2*)(to + l.lo) = *(u32x2*)(to + l.hi) = u32x2{0, 0};
+    }
+    return;
+  }
   const float rs = ACC ? A.row_scale[token] : 1.0f;
   float gq[8], gk[8];
   l.angles(A, j, pos);
@@ -396,6 +403,7 @@ static HeadArgs head_args(const nm_heads_problem_t& p, const void* gamma_q, cons
   a.dim = p.head_dim;
   a.rotary = p.rotary_dim;
   a.eps = p.eps;
+  a.zero_rows = p.zero_rows;
   a.rdim = (float)(1.0 / (double)p.head_dim);
   return a;
 }
@@ -432,6 +440,7 @@ nm_status_t nm_heads_plan_init(nm_heads_plan_t* plan, const nm_heads_problem_t* 
   if (p->pairs != NM_PAIRS_HALVES && p->pairs != NM_PAIRS_NEIGHBOURS)
     return layer_fail(NM_ERR_INVALID_ARG, "pairs must be NM_PAIRS_HALVES or NM_PAIRS_NEIGHBOURS");
   if (!(isfinite(p->eps) && p->eps >= 0.0f)) return layer_fail(NM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (p->zero_rows != 0 && p->zero_rows != 1) return layer_fail(NM_ERR_INVALID_ARG, "zero_rows must be 0 or 1");
   if (p->rows < 0 || p->rows >= ((int64_t)1 << 24)) return layer_fail(NM_ERR_SHAPE, "rows must be >= 0 and < 2^24");
   if (p->heads_q < 1 || p->heads_k < 0 || p->heads_v < 0 || p->heads_q > 65536 || p->heads_k > 65536 || p->heads_v > 65536)
     return layer_fail(NM_ERR_SHAPE, "heads_q must be 1 to 65536, heads_k and heads_v 0 to 65536");

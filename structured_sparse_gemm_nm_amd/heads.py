@@ -4,7 +4,9 @@
 or ``Rows`` of int32 accumulators, and runs nm_head_norm_rope in one pass. From
 16-bit rows it is differentiable in the rows and in both gains
 (nm_head_norm_rope_backward), so it stands between a SemiStructuredSparseLinear and
-the attention in training too.
+the attention in training too. A backward pass may be captured into a graph while no
+eager graph of the same leaves lives: torch ties their gradients to the stream of
+the first.
 """
 import torch
 from torch.autograd.function import once_differentiable
@@ -40,7 +42,7 @@ def _plan(x, heads, dim, table, gamma, pairs, eps):
     key = (x.shape[0], x.stride(0), heads, dim, rotary, table_rows, gamma.dtype, acc, pairs, eps)
     return _PLANS.get(key, lambda: nm_heads_plan_init(
         x.shape[0], *heads, dim, rotary, pairs=pairs, table_rows=table_rows, dtype=_DTYPE_NAMES[gamma.dtype],
-        x_dtype="i32" if acc else None, ldx=x.stride(0), eps=eps))
+        x_dtype="i32" if acc else None, ldx=x.stride(0), eps=eps, zero_rows=True))
 
 
 class _NormRotate(torch.autograd.Function):
@@ -48,7 +50,7 @@ class _NormRotate(torch.autograd.Function):
     def forward(ctx, x, gamma_q, gamma_k, positions, table, heads, pairs, eps):
         x = _rows_on_16_bytes(x)
         plan = _plan(x, heads, gamma_q.shape[0], table, gamma_q, pairs, eps)
-        y = torch.zeros(x.shape, dtype=x.dtype, device=x.device)       # rows without a token are not written
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         nm_head_norm_rope(plan, x, gamma_q, gamma_k, positions, table, y)
         ctx.save_for_backward(x, gamma_q, gamma_k, positions, table)
         ctx.plan = plan
@@ -92,14 +94,14 @@ def norm_rotate(x, gamma_q, gamma_k, positions, table, heads, pairs="halves", ep
     if table is not None and table.dim() != 2:
         raise ValueError("table must be positions x rotary_dim")
     wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (v, gamma_q, gamma_k, *x[1:]))
+    if torch.is_grad_enabled() and table is not None and table.requires_grad:
+        raise RuntimeError("the table has no gradient")
     if not acc and wants:
-        if table is not None and table.requires_grad:
-            raise RuntimeError("the table has no gradient")
         return _NormRotate.apply(v, gamma_q, gamma_k, positions, table, heads, pairs, eps)
     if wants:
         raise RuntimeError("accumulators have no gradient: detach the gains, or call it under torch.no_grad()")
     v = _rows_on_16_bytes(v)
     plan = _plan(v, heads, gamma_q.shape[0], table, gamma_q, pairs, eps)
-    y = torch.zeros(v.shape, dtype=gamma_q.dtype, device=v.device)
+    y = torch.empty(v.shape, dtype=gamma_q.dtype, device=v.device)
     nm_head_norm_rope(plan, v, gamma_q, gamma_k, positions, table, y, row_scale=x.row_scale, col_scale=x.col_scale)
     return y

@@ -92,12 +92,12 @@ def cuda(t):
     return None if t is None else t.cuda()
 
 
-def run(s, pairs, eps=1e-6, pad=0, in_place=False, table=True):
+def run(s, pairs, eps=1e-6, pad=0, in_place=False, table=True, zero_rows=False):
     rows, cols = s["x"].shape
     ld, acc = up16(cols) + pad, s["row_scale"] is not None
     x, _ = strided(s["x"], ld, 77)
     plan = nm.nm_heads_plan_init(rows, *s["heads"], s["dim"], s["rotary"], pairs=pairs, table_rows=s["table"].shape[0],
-                                 dtype=s["dtype"], x_dtype="i32" if acc else None, ldx=ld, ldy=ld, eps=eps)
+                                 dtype=s["dtype"], x_dtype="i32" if acc else None, ldx=ld, ldy=ld, eps=eps, zero_rows=zero_rows)
     out = Out(rows, cols, ld, TORCH[s["dtype"]])
     y = x if in_place else out.t
     nm.nm_head_norm_rope(plan, x, s["gamma_q"].cuda(), s["gamma_k"].cuda(), s["positions"].cuda(),
@@ -204,6 +204,16 @@ def test_rows_without_a_token_stay_as_they_were(acc):
     y = run(s, "halves")[0]
     out = s["positions"].cuda() < 0
     assert (y[out] == 93).all() and torch.equal(y[~out], whole[~out])
+
+
+@pytest.mark.parametrize("rows,heads,dim", [(3, (5, 1, 1), 80), (400, (20, 3, 2), 512), (70, (1, 0, 0), 8)])
+@pytest.mark.parametrize("acc", [False, True])
+def test_rows_without_a_token_become_zeros(rows, heads, dim, acc):
+    s = inputs(rows, heads, dim, dim, "bf16", acc)
+    y, _, _, _ = run(s, "halves")
+    s["positions"][::2] = -1 - torch.arange(0, rows, 2) * (1 << 40)
+    z, _, _, _ = run(s, "halves", zero_rows=True)
+    assert (z[::2] == 0).all() and torch.equal(z[1::2], y[1::2])
 
 
 def test_a_position_behind_the_table_is_nan():
@@ -326,6 +336,8 @@ def test_wrapper_refuses():
             norm_rotate(*args)
     with pytest.raises(RuntimeError, match="gradient"):
         norm_rotate(rows, gq.clone().requires_grad_(), gq, at, table, (2, 1, 1))
+    with pytest.raises(RuntimeError, match="gradient"):
+        norm_rotate(rows, gq, gq, at, table.clone().requires_grad_(), (2, 1, 1))
     with pytest.raises(RuntimeError, match="gradient"):
         norm_rotate(rows.dense().half().requires_grad_(), gq, gq, at, table.clone().requires_grad_(), (2, 1, 1))
 

@@ -42,6 +42,8 @@ def test_plan_accepts():
     p.rows, p.heads_q, p.head_dim, p.ldx, p.ldy, p.pairs = 1, 1, 8, 8, 8, 2
     h = ctypes.c_void_p()
     assert nm.lib().nm_heads_plan_init(ctypes.byref(h), ctypes.byref(p)) == nm.NM_ERR_INVALID_ARG and h.value is None
+    p.pairs, p.type_io, p.type_x, p.zero_rows = 0, nm.NM_F16, nm.NM_F16, 2
+    assert nm.lib().nm_heads_plan_init(ctypes.byref(h), ctypes.byref(p)) == nm.NM_ERR_INVALID_ARG and h.value is None
     assert nm.lib().nm_heads_plan_init(None, ctypes.byref(p)) == nm.NM_ERR_INVALID_ARG
     assert nm.lib().nm_heads_plan_init(ctypes.byref(h), None) == nm.NM_ERR_INVALID_ARG
 
