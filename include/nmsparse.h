@@ -462,7 +462,7 @@ typedef struct {
   int32_t type_x;           /* NM_F16, NM_BF16, NM_F32 or NM_I32 */
   int32_t top;              /* alternatives a row: 0 to 32, at most cols */
   int64_t ldx, ldg;         /* rows of x, and of its gradient (not read for NM_I32) */
-  float scale;              /* one over the temperature: finite and > 0 */
+  float scale;              /* one over the temperature: > 0, at most 2^127 */
 } nm_logprobs_problem_t;
 typedef struct nm_logprobs_plan* nm_logprobs_plan_t;
 nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_problem_t* problem);
@@ -484,8 +484,9 @@ nm_status_t nm_logprobs(nm_logprobs_plan_t plan, const void* dX, const float* d_
  *   dx_i = scale * (g * ([i == token] - p_i) - h * p_i * (log p_i + H)).
  * One of d_grad_logprob (with d_tokens) and d_grad_entropy (with d_entropy, the
  * forward's) may be NULL: that term is left out. A row whose token is none has no g, a
- * row of -infinity alone gradient 0. d_stats comes from nm_logprobs on the same x and
- * scale. d_grad_x may equal dX where ldg == ldx. */
+ * row of -infinity alone gradient 0, and so has a row whose g and h are 0 or left out,
+ * whatever its logits (a padded row's may be NaN). d_stats comes from nm_logprobs on
+ * the same x and scale. d_grad_x may equal dX where ldg == ldx. */
 nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const int64_t* d_tokens, const float* d_stats,
                                  const float* d_entropy, const float* d_grad_logprob, const float* d_grad_entropy,
                                  void* d_grad_x, void* stream);

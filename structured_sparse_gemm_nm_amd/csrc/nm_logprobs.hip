@@ -600,7 +600,8 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
   if (logs == INFINITY) g = 0.0f;                 // no weight in the row
   float h = 0.0f, H = 0.0f;
   if constexpr (ENT) { h = A.g_entropy[row]; H = A.entropy[row]; }
-  const float own = A.scale * g, g2 = -A.scale * __builtin_fmaf(h, H, g), h2 = -A.scale * h * 0.693147180559945f;
+  const bool none = g == 0.0f && h == 0.0f;       // zeros, also where the logits are NaN
+  const float own = A.scale * g, g2 = none ? 0.0f : -A.scale * __builtin_fmaf(h, H, g), h2 = -A.scale * h * 0.693147180559945f;
   const float logs2 = logs * 1.44269504088896f;
 #pragma unroll
   for (int u = 0; u < U; u++) {
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
     // with the token's own term where it is: - scale (g + h (log p + H)) p, its logs in base 2
 #pragma unroll
     for (int i = 0; i < LP_V; i++) {
-      const float lp = __builtin_fmaf(x[i] - m, A.scale2, -logs2), p = __builtin_amdgcn_exp2f(lp);
+      const float lp = none ? -INFINITY : __builtin_fmaf(x[i] - m, A.scale2, -logs2), p = __builtin_amdgcn_exp2f(lp);
       x[i] = p * (ENT ? __builtin_fmaf(h2, fmaxf(lp, -300.0f), g2) : g2);
     }
     const uint64_t at = (uint64_t)(token - c);
@@ -701,7 +702,7 @@ nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_pr
   if (!p) return layer_fail(NM_ERR_INVALID_ARG, "problem is NULL");
   if (p->type_x != NM_F16 && p->type_x != NM_BF16 && p->type_x != NM_F32 && p->type_x != NM_I32)
     return layer_fail(NM_ERR_INVALID_ARG, "type_x must be NM_F16, NM_BF16, NM_F32 or NM_I32");
-  if (!(isfinite(p->scale) && p->scale > 0.0f)) return layer_fail(NM_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!(p->scale > 0.0f && p->scale <= 0x1p127f)) return layer_fail(NM_ERR_INVALID_ARG, "scale must be > 0 and at most 2^127");
   if (p->rows < 0 || p->rows >= ((int64_t)1 << 24)) return layer_fail(NM_ERR_SHAPE, "rows must be >= 0 and < 2^24");
   if (p->cols < 1 || p->cols > ((int64_t)1 << 22)) return layer_fail(NM_ERR_SHAPE, "cols must be 1 to 2^22");
   if (p->top < 0 || p->top > LP_TOP || p->top > p->cols)

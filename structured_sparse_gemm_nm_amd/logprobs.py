@@ -4,7 +4,9 @@
 accumulators that the head's product handed on, and runs nm_logprobs. From 16-bit or
 fp32 logits the log probabilities and the entropy are differentiable
 (nm_logprobs_backward): minus their mean is the loss that a language model is trained
-on, the entropy a term beside it.
+on, the entropy a term beside it. A backward pass may be captured into a graph while no
+eager graph of the same leaves lives: torch ties their gradients to the stream of
+the first.
 """
 from typing import NamedTuple, Optional
 

@@ -211,6 +211,30 @@ def test_masks(rows, cols, dtype):
     assert call(s, 4)[2]["logprob"][4] == 0
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("cols", [5, 2500])
+def test_padded_rows_have_gradient_zero(cols, dtype):
+    """Whatever lies in them: their tokens are none, and the entropy's gradient is 0 or left out."""
+    s = inputs(6, cols, dtype, 3)
+    s["x"][1], s["x"][3, cols // 2], s["x"][4, 0] = math.nan, INF, math.nan
+    s["tokens"][1:5], s["h"][1:5] = torch.tensor([-1, -100, -1, -1]), torch.tensor([0.0, 0.0, -0.0, 0.0])
+    plan, xg, out = call(s)
+    for h in (False, True):
+        dx = backward(s, plan, xg, out, h=h)
+        assert (dx[1:5] == 0).all() and (dx[0] != 0).any() and (dx[5] != 0).any()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** -126])
+def test_the_scale_at_its_bounds(scale):
+    """Nothing but the largest logit is left, or all alike; the next logits are 1 below it, times 2^127 still finite."""
+    x = torch.tensor([[0.0, -1.0, -2.0 ** -20, -1.0] * 100, [3.0] + [2.0] * 399], device="cuda")
+    plan = nm.nm_logprobs_plan_init(2, 400, dtype="f32", scale=scale)
+    out, H, at = torch.empty(2, device="cuda"), torch.empty(2, device="cuda"), torch.tensor([4, 0], device="cuda")
+    nm.nm_logprobs(plan, x, at, out, entropy=H, workspace=plan.empty_workspace())
+    want = torch.tensor([100.0, 1.0] if scale > 1 else [400.0, 400.0]).log()
+    assert torch.allclose(out.cpu(), -want, rtol=1e-6, atol=1e-6) and torch.allclose(H.cpu(), want, rtol=1e-6, atol=1e-6)
+
+
 @pytest.mark.parametrize("scale", [1.0, 3.0])
 def test_a_token_ruled_out(scale):
     s = inputs(4, 100, "f32", 8)

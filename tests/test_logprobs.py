@@ -18,6 +18,7 @@ def plan(**kw):
     (dict(cols=(1 << 22) + 8), nm.NM_ERR_SHAPE), (dict(top=-1), nm.NM_ERR_SHAPE), (dict(top=33), nm.NM_ERR_SHAPE),
     (dict(cols=16, top=17), nm.NM_ERR_SHAPE), (dict(scale=0.0), nm.NM_ERR_INVALID_ARG), (dict(scale=-1.0), nm.NM_ERR_INVALID_ARG),
     (dict(scale=math.nan), nm.NM_ERR_INVALID_ARG), (dict(scale=math.inf), nm.NM_ERR_INVALID_ARG),
+    (dict(scale=2.0 ** 127 * 1.01), nm.NM_ERR_INVALID_ARG),
     (dict(ldx=63), nm.NM_ERR_SHAPE), (dict(ldg=63), nm.NM_ERR_SHAPE), (dict(ldx=68), nm.NM_ERR_ALIGN),
     (dict(ldg=68), nm.NM_ERR_ALIGN), (dict(dtype="f32", ldx=66), nm.NM_ERR_ALIGN), (dict(cols=1003), nm.NM_ERR_ALIGN),
     (dict(ldx=1 << 47), nm.NM_ERR_SHAPE),
@@ -27,7 +28,7 @@ def test_plan_refuses(kw, status):
 
 
 def test_plan_accepts():
-    plan(cols=1), plan(cols=7, top=7), plan(rows=0), plan(dtype="f32", ldx=68), plan(dtype="i32", ldg=1), plan(cols=1 << 22, top=32)
+    plan(scale=2.0 ** 127), plan(scale=2.0 ** -140), plan(cols=1), plan(cols=7, top=7), plan(rows=0), plan(dtype="f32", ldx=68), plan(dtype="i32", ldg=1), plan(cols=1 << 22, top=32)
     with pytest.raises(ValueError):
         plan(dtype="i8")
     p = nm.nm_logprobs_problem_t()
