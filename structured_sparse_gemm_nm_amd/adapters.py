@@ -48,7 +48,7 @@ class Adapters:
         tokens x out of the shared product, a 16-bit tensor or ``Rows``. Returns 16-bit rows: out, which may be base, or
         new ones."""
         base = base if isinstance(base, Rows) else Rows(base)
-        for t in (x, x_scale, *base):
+        for t in (x, x_scale, *base, out):
             if torch.is_grad_enabled() and t is not None and t.requires_grad:
                 raise RuntimeError("adapters that are served have no backward pass: detach the operands, or call it "
                                    "under torch.no_grad()")

@@ -261,6 +261,8 @@ def test_wrapper(dtype):
     assert torch.equal(y[1], base[1]) and torch.equal(y[6], base[6])
     with pytest.raises(RuntimeError, match="backward"):
         ad.add(x.clone().requires_grad_(), index, base)
+    with pytest.raises(RuntimeError, match="backward"):
+        ad.add(x, index, base, out=torch.empty((9, 64), dtype=dtype, device="cuda", requires_grad=True)[:, :60])
     for bad in (dict(x=x.float()), dict(x=x[:, :50]), dict(index=index.int()), dict(index=index[:3]), dict(base=base[:, :30]),
                 dict(base=base.float()), dict(x=x.cpu()), dict(base=Rows(base, index.float(), None)), dict(x=x[0])):
         with pytest.raises((ValueError, nm.NmError)):
