@@ -89,12 +89,12 @@ __device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0, int&
 // counts' sums, and the tokens put behind them. Adapters 4096 apart share a bin, and a tile holds
 // whatever it gets: the order is for speed alone. One block; the order within a bin is that in
 // which the atomics are served, and no token's result depends on it: each is a column of its own.
-// It takes 4 us with its launch, at 65 tokens as at 4096 (latency: the index, places, sums, the
+// It takes 4 us with its launch, at 256 tokens as at 4096 (latency: the index, places, sums, the
 // order), which a prompt in runs pays for nothing: 4096 tokens, 64 adapters of rank 16, k = m =
-// 4096, bf16, in runs 26.0 us without it and 29.7 with it, scattered 207 and 37.3. So it runs from
-// where scattered tokens gain about that: 256 tokens over 64 adapters 34.7 us without and 27.5
-// with, over 8 14.6 and 16.3; 1024 over 8 29.8 and 23.5, over 4 23.1 and 23.4; 4096 over 4 40.8
-// and 30.7, over 2 30.9 and 30.8; 128 over 64 16.1 and 18.5.
+// 4096, bf16, in runs 24.5 us without it and 27.9 with it, scattered 174 and 34.8. So it runs from
+// where scattered tokens gain about that: 256 tokens over 64 adapters 26.4 us without and 22.9
+// with, over 8 12.0 and 16.3; 1024 over 8 28.4 and 23.2, over 4 22.3 and 23.4; 4096 over 4 33.7
+// and 29.8, over 2 27.6 and 30.8; 128 over 64 15.1 and 18.5.
 __global__ void __launch_bounds__(LORA_SORT_THREADS) lora_sort_kernel(LoraArgs A, intx2* order) {
   constexpr int T = LORA_SORT_THREADS, B = LORA_SORT_BINS / T, U = 4;
   __shared__ int bins[LORA_SORT_BINS];
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
       bool in[NT];
 #pragma unroll
       for (int j = 0; j < NT; j++) {
+        if (j > 0 && c0 + 16 * j >= cols.count) break;    // most groups of a prompt's scattered tokens are small
         in[j] = cols.has(c0 + 16 * j + l16);
         token[j] = cols.token(c0 + 16 * j + l16);
         rs[j] = ACC ? A.row_scale[token[j]] : 1.0f;
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
       }
       if (adapter >= 0) {
 #pragma unroll 1
-        for (int e = threadIdx.x; e < 16 * NT * PER; e += THREADS) {
+        for (int e = threadIdx.x; e < min(16 * NT, (cols.count - c0 + 15) / 16 * 16) * PER; e += THREADS) {
           const int j = e / PER, r = e % PER * 4;
           if (A.x_scale) xs = A.x_scale[cols.token(c0 + j)];
           floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -620,10 +621,13 @@ nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* p) 
   pl->p = *p;
   pl->tiles = (int)((p->n + LORA_TILE - 1) / LORA_TILE);
   const int64_t tile = p->n < LORA_TILE ? p->n : LORA_TILE, tiles = pl->tiles ? pl->tiles : 1;
-  // a block for each token of a tile while that are few, then fewer for its groups
+  // A block for each token of a tile while that are few, then fewer for its groups. With 64 adapters of rank 16, k = m =
+  // 4096, scattered, in us: up to 4096 blocks 256 tokens 27.1 and 4096 tokens 36, up to 16384 26.4 and 67, runs of 256
+  // tokens 15.4 and 20.5; then 512 over the tiles 256 tokens 23.1 and 4096 34.9, 256 24.6 and 37.3, 1024 27.2 and 35.9,
+  // 2048 34.8 and 37.3.
   auto slots = [&](int64_t blocks) {
     if (blocks * tile <= 4096) return (int)tile;
-    const int64_t want = 1024 / blocks;
+    const int64_t want = 512 / blocks;
     return (int)(want < 1 ? 1 : want > tile ? tile : want);
   };
   const int rank_tiles = (p->rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
