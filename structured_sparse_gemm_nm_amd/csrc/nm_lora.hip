@@ -373,7 +373,9 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
   constexpr int NS = SETS == 0 ? 1 : SETS;
   constexpr int RANKS = SETS == 0 ? 16 : 32 * SETS;
   constexpr int PER = RANKS / 4;                          // threads that bring a token's t
-  constexpr int WS = 4;                                   // parts of t on their way together
+  // Parts of t on their way together. In us with 4 and 8: k = 16384, m = 4096, rank 64, 8 tokens 12.1 and 11.2; rank 128,
+  // 37 tokens of k = 11008 27.6 and 30.6; rank 16, 16 tokens of k = 4096 10.4 and 10.8, 4096 tokens 44.9 and 51.1.
+  constexpr int WS = NT == 1 && SETS == 2 ? 8 : 4;
   constexpr int BQ = ACC ? 2 : 1;                         // pieces of 16 bytes a lane's outputs take of the base
   __shared__ uint16_t ts[16 * NT][2 * RANKS + 8];         // both parts of t; 16 tokens lie on distinct banks
   __shared__ float factor[16 * NT];
@@ -632,8 +634,12 @@ nm_status_t nm_lora_plan_init(nm_lora_plan_t* plan, const nm_lora_problem_t* p) 
   };
   const int rank_tiles = (p->rank + 15) / 16, across = rank_tiles <= 1 ? 1 : rank_tiles <= 2 ? 2 : rank_tiles <= 4 ? 4 : 8;
   const int64_t step = (int64_t)LORA_KW * (LORA_WAVES / across), steps = (p->k + step - 1) / step;
+  // Parts of k, each of which the outer product reads t of. 32 instead of 16 for a few tokens: one token, k = 65536, rank
+  // 128 28.4 us instead of 44.4, 8 tokens, k = 16384, rank 64 12.1 and 12.5; but 16 tokens of 32 adapters, k = 11008, rank
+  // 64 14.2 instead of 12.3, 64 tokens of rank 32 18.5 and 16.3.
+  const int64_t parts = p->n <= 8 ? 32 : 16;
   int64_t splits = 1024 / tiles;
-  if (splits > 16) splits = 16;
+  if (splits > parts) splits = parts;
   if (splits > steps) splits = steps;
   if (splits < 1) splits = 1;
   pl->loops = (int)((steps + splits - 1) / splits);
