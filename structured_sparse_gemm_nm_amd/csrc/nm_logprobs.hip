@@ -26,13 +26,14 @@ namespace nm {
 
 constexpr int LP_V = 8;              // columns a thread takes at a time
 constexpr int LP_THREADS = 256;
-constexpr int LP_JOIN = 512;         // where the slices' alternatives are joined
-constexpr int LP_U = 2;              // pieces a thread takes at a time
+constexpr int LP_JOIN = 512;         // most threads where the slices' alternatives are joined
+constexpr int LP_U = 2;              // pieces a thread takes at a time: 4096 x 131072 508 us, with 1 513; accumulators 60, with 4 77
 constexpr int LP_TOP = 32;           // most alternatives
 constexpr int LP_ROUNDS = 8;        // of 64 columns that a wave looks through together
 constexpr int LP_CAP = 128;          // candidates a wave holds
 constexpr int LP_CHUNKS = 2048;      // most groups of columns whose largest are kept for the alternatives
-constexpr int LP_MOST_SLICES = 64;
+constexpr int LP_ALL = LP_CHUNKS / LP_JOIN;   // of them a thread of the join keeps, all of a row's
+constexpr int LP_MOST_SLICES = 32;   // 16 rows of 131072 fp32 logits with 20 alternatives 11.8 us, 64 slices 13.1, 16 12.8
 constexpr int64_t LP_LONGEST = 1 << 17;   // columns a slice: a thread's chain of sums stays under 64 pieces
 
 enum LpType { LP_F16 = 0, LP_BF16 = 1, LP_F32 = 2, LP_I32 = 3 };
@@ -51,7 +52,7 @@ struct LpArgs {
   float* largest;         // rows x chunks: the largest logits of the threads' groups
   int64_t rows, cols, ldx, slice;
   int slices, top;
-  int group;              // neighbouring threads whose columns are one chunk: 1, 4 or 16
+  int group;              // neighbouring threads whose columns are one chunk: 1 or 4
   float scale, scale2;    // scale2 = scale * log2(e)
 };
 
@@ -440,6 +441,10 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
 }
 
 // One block a slice of a row, LP_U pieces a thread at a time and the next ones on their way.
+// Memory bounds it: 4096 x 131072 bf16, 1.07 GB, 199 us, 5.4 TB/s; 2048 x 32768 accumulators,
+// 268 MB, 57 us, 4.7 TB/s. A logit costs a multiply-add, an exponential, an addition, half a
+// maximum and its conversion, and with the entropy two more: a change of the largest, which
+// scales the sums, comes once for LP_U pieces at most and rarely after the first.
 template <int XT, bool ENT, bool TOP, bool STREAM>
 __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -528,13 +533,9 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
     if (threadIdx.x == blockDim.x - 1) lp_write(A, row, t, token, given);    // the first wave has the alternatives
   } else {
     if constexpr (TOP) {
-      if (A.group >= 4) {
+      if (A.group == 4) {
         mine = fmaxf(mine, lane_dpp<0xB1>(mine));
         mine = fmaxf(mine, lane_dpp<0x4E>(mine));
-      }
-      if (A.group >= 16) {
-        mine = fmaxf(mine, lane_dpp<0x141>(mine));
-        mine = fmaxf(mine, lane_dpp<0x140>(mine));
       }
       if (threadIdx.x % A.group == 0) A.largest[(block * LP_THREADS + threadIdx.x) / A.group] = mine;
     }
@@ -543,7 +544,9 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
   }
 }
 
-// The slices of a row joined; one wave a row where there are no alternatives.
+// The slices of a row joined; one wave a row where there are no alternatives. Latency bounds it:
+// 6.0 us for 32003 logits and 5 alternatives, about 8 for 16 rows of 131072 and 20 (the largest of
+// the chunks, their columns, the lists: one behind the other).
 template <int XT, bool TOP>
 __global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
   const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -560,11 +563,11 @@ __global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
     __shared__ float largest[LP_CHUNKS];
     const int chunks = A.slices * (LP_THREADS / A.group);
     const float* const from = A.largest + row * chunks;
-    float v[LP_CHUNKS / LP_JOIN];
+    float v[LP_ALL];
 #pragma unroll
-    for (int i = 0; i < LP_CHUNKS / LP_JOIN; i++) v[i] = from[min((int)threadIdx.x + i * LP_JOIN, chunks - 1)];
+    for (int i = 0; i < LP_ALL; i++) v[i] = from[min((int)threadIdx.x + i * (int)blockDim.x, chunks - 1)];
 #pragma unroll
-    for (int i = 0; i < LP_CHUNKS / LP_JOIN; i++) largest[threadIdx.x + i * LP_JOIN] = v[i];
+    for (int i = 0; i < LP_ALL; i++) largest[threadIdx.x + i * blockDim.x] = v[i];
     t = lp_join<LP_JOIN / 64>(t, A.scale2);
     __syncthreads();
     LpTop top;
@@ -578,7 +581,8 @@ __global__ void __launch_bounds__(LP_JOIN) lp_join_kernel(LpArgs A) {
 
 // dx_i = scale (g [i = t] - p_i (g + h (log p_i + H))), g and h the gradients of the
 // row's log probability and entropy H; p_i from the forward's largest and sum. Below
-// 2^-300 p is 0 in fp32, and the log is held there for infinite ones.
+// 2^-300 p is 0 in fp32, and the log is held there for infinite ones. Memory bounds it:
+// 4096 x 131072 bf16, 2.1 GB, 343 us, 6.3 TB/s.
 template <int XT, bool ENT, bool STREAM>
 __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
   constexpr int U = 4;
@@ -659,15 +663,23 @@ static dim3 lp_grid(int64_t blocks) {
   return dim3((unsigned)across, (unsigned)((blocks + across - 1) / across));
 }
 
-// Logits that the caches do not hold until they are read again (256 MB on this card) are read past them.
+// Logits that the caches do not hold until they are read again (256 MB on this card) are read past them, and so is
+// their gradient written: 4096 x 131072 bf16 (1 GB) forward and backward 566 us without, 522 with loads and 509 with
+// stores past them; 2048 x 32768 accumulators (268 MB) 60 us without and 66 with.
 static bool lp_streams(int64_t rows, int64_t cols, int size) { return rows * cols * size >= (int64_t)1 << 29; }
+
+// Half the threads where that keeps the chunks' list: 32003 f16 logits with 5 alternatives 9.7 us, 10.3 with all; but 16
+// rows of 131072 12.4 with half where there are 2048 chunks, 11.8 with all, and 1024 threads are slower for both (12.8, 15.5).
+static unsigned lp_join_threads(const LpArgs& a) {
+  return a.slices * (LP_THREADS / a.group) <= LP_ALL * LP_JOIN / 2 ? LP_JOIN / 2 : LP_JOIN;
+}
 
 template <int XT, bool ENT, bool TOP>
 hipError_t lp_go(const LpArgs& a, int threads, hipStream_t s) {
   const dim3 grid = lp_grid(a.rows * a.slices);
   if (lp_streams(a.rows, a.cols, LP_SIZE<XT>)) hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP, true>), grid, dim3((unsigned)threads), 0, s, a);
   else hipLaunchKernelGGL((lp_kernel<XT, ENT, TOP, false>), grid, dim3((unsigned)threads), 0, s, a);
-  if (a.slices > 1) hipLaunchKernelGGL((lp_join_kernel<XT, TOP>), lp_grid(a.rows), dim3(TOP ? LP_JOIN : 64), 0, s, a);
+  if (a.slices > 1) hipLaunchKernelGGL((lp_join_kernel<XT, TOP>), lp_grid(a.rows), dim3(TOP ? lp_join_threads(a) : 64), 0, s, a);
   return hipGetLastError();
 }
 
@@ -714,7 +726,8 @@ nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_pr
   nm_logprobs_plan* pl = new (std::nothrow) nm_logprobs_plan();
   if (!pl) return layer_fail(NM_ERR_INVALID_ARG, "out of host memory");
   pl->p = *p;
-  // Slices: four blocks a CU where the row has a whole round of pieces for each.
+  // Slices: four blocks a CU where the row has a whole round of pieces for each. 256 rows of 131072 fp32 logits 33.6 us;
+  // with two blocks a CU 36.1, with one 46.3, with eight 33.2; 64 rows 17.7, 17.0, 19.2, 17.0.
   const int64_t pieces = (p->cols + LP_V - 1) / LP_V, rounds = (pieces + LP_THREADS - 1) / LP_THREADS;
   int64_t n = p->rows ? (1024 + p->rows - 1) / p->rows : 1;
   if (n > rounds) n = rounds;
@@ -725,7 +738,7 @@ nm_status_t nm_logprobs_plan_init(nm_logprobs_plan_t* plan, const nm_logprobs_pr
   pl->slices = (int)((pieces + pl->slice - 1) / pl->slice);
   pl->threads = pl->slices > 1 || pieces >= LP_THREADS ? LP_THREADS : (int)((pieces + 63) / 64 * 64);
   const int64_t all = (int64_t)pl->slices * pl->threads;
-  pl->group = all <= LP_CHUNKS ? 1 : all <= 4 * LP_CHUNKS ? 4 : 16;
+  pl->group = all <= LP_CHUNKS ? 1 : 4;                    // LP_MOST_SLICES blocks of LP_THREADS are 4 LP_CHUNKS
   *plan = pl;
   return layer_fail(NM_OK, "");
 }
