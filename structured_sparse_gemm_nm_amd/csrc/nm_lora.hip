@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
 // SETS: chunks of eight ranks a lane takes; 0: up to 16 ranks, both parts in one instruction.
 // Memory bounds it for prompts: 4096 tokens to 6144 features beside accumulators, 151 MB, 33 us,
 // 4.6 TB/s (with 64 outputs a wave 40 us: half the waves); for few tokens latency, 3.4 us for one
-// and 6.4 for 16 tokens to 22016 features (13 MB). Eight of the 60 variants spill 4 to 23 registers,
+// and 6.4 for 16 tokens to 22016 features (13 MB). Seven of the 64 variants spill 4 to 23 registers,
 // ranks over 64 beside accumulators most: their loads are in flight together.
 template <int IO, bool ACC, int SETS, int NT, bool OWN, int FB>
 __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs A) {
