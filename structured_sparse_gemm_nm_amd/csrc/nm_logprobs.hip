@@ -382,7 +382,12 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
     for (int u = 0; u < 8; u++) most = i + 64 * u < chunks ? fmaxf(most, v[u]) : most;
   }
   t.init(lds.keys[wave], A.top);
-  t.value = lp_nth(most, A.top, (float*)lds.keys[wave]);
+  const float bound = lp_nth(most, A.top, (float*)lds.keys[wave]);
+  t.value = bound;
+  // Where half the lanes' largest are the bound itself, most columns may be (logits ruled out with one value): chunks are
+  // then looked through for larger ones alone, and the lowest columns of the bound are found from the row's start on.
+  // 16 rows of 131072 of -infinity, 20 alternatives: 21 us, 109 without; of random logits 12.0 and 11.8.
+  const bool flood = __popcll(__ballot(most == bound)) >= 32;
   // this wave's chunks
   int* const list = lds.chunks[wave];
   int count = 0;
@@ -394,7 +399,7 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
 #pragma unroll
     for (int u = 0; u < 4; u++) {
       const int at = b + 64 * waves * u;
-      const bool holds = at < chunks && v[u] >= t.value;
+      const bool holds = at < chunks && (flood ? v[u] > bound : v[u] >= bound);
       const uint64_t mask = __ballot(holds);
       if (holds) list[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0))] = at;
       count += __popcll(mask);
@@ -426,7 +431,7 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
     }
 #pragma unroll
     for (int u = 0; u < LP_ROUNDS; u++)
-      if (!(x[u] >= t.value)) hold &= ~(1u << u);
+      if (!(x[u] >= t.value) || (flood && x[u] == bound)) hold &= ~(1u << u);
     while (__any(hold != 0)) {                             // one a lane at a time: few reach the bound
       const int u = __builtin_ctz(hold | 1u << 31);
       float v = x[0];
@@ -435,6 +440,21 @@ __device__ __forceinline__ void lp_alternatives(LpTop& t, const LpArgs& A, const
       int piece;
       t.add(lp_key(v, (uint32_t)column(b + 64 * u, piece)), hold != 0);
       hold &= hold - 1;
+    }
+  }
+  if (flood && wave == 0) {
+    int found = 0;
+#pragma unroll 1
+    for (int64_t b = lane; b - lane < A.cols && found < A.top; b += LP_ROUNDS * 64) {
+      float x[LP_ROUNDS];
+#pragma unroll
+      for (int u = 0; u < LP_ROUNDS; u++) x[u] = lp_one<XT>(xr, A.col_scale, rs, min(b + 64 * u, A.cols - 1));
+#pragma unroll
+      for (int u = 0; u < LP_ROUNDS; u++) {
+        const bool holds = b + 64 * u < A.cols && x[u] == bound;
+        if (found < A.top) t.add(lp_key(x[u], (uint32_t)(b + 64 * u)), holds);
+        found += __popcll(__ballot(holds));
+      }
     }
   }
   lp_top_join<W>(t, lds.keys, lds.counts);
@@ -459,6 +479,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
   const float given = A.slices == 1 ? lp_given<XT>(A, row, token) : 0.0f;
 
   LpSum t = {-FLT_MAX, 0.0f, 0.0f, -FLT_MAX, 0.0f};
+  float mine = -INFINITY;                         // the thread's largest: t.m, or below it where that is none's
   auto take = [&](const LpRaw<XT> (&raw)[LP_U], int b) {
     float x[LP_U][LP_V], most = -INFINITY;
 #pragma unroll
@@ -475,6 +496,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
 #pragma unroll
       for (int i = 0; i < LP_V; i += 2) most = lp_max3(most, x[u][i], x[u][i + 1]);
     }
+    if constexpr (TOP) mine = fmaxf(mine, most);
     if (most > t.m) lp_shift(t, most, A.scale2, true);
     const bool near = lp_near(t.ms);
 #pragma unroll
@@ -514,9 +536,6 @@ __global__ void __launch_bounds__(LP_THREADS) lp_kernel(LpArgs A) {
     take(next, b + step);
   }
 
-  // -FLT_MAX stands for nothing but -infinity; a row's lowest logit may be it, and then
-  // counts as less than it is, which keeps the bound of the alternatives' chunks
-  float mine = t.m == -FLT_MAX ? -INFINITY : t.m;
   if (A.slices == 1) {
     if constexpr (TOP) {
       __shared__ LpLists<LP_THREADS / 64> lds;

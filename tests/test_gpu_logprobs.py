@@ -212,6 +212,29 @@ def test_masks(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 513), (1, 32003), (7, 2048), (3, 140001), (1100, 4100)])
+def test_alternatives_among_logits_ruled_out(rows, cols, dtype):
+    """Few logits are left, or all but the last columns' are equal, or two low values mix: the lowest columns come next."""
+    s = inputs(rows, cols, dtype, cols)
+    x, low = s["x"], torch.finfo(TORCH[dtype]).min
+    g = gen(5)
+    for row in range(min(rows, 7)):
+        kept = torch.randperm(cols, generator=g)[:(0, 1, 3, 19, 20, 40, 7)[row]]
+        values = x[row, kept].clone()
+        x[row] = -INF if row % 2 else low
+        if row == 4:
+            x[row, cols // 2:] = -INF
+        if row == 5:
+            x[row, cols - 9:] = low                     # the larger of the low ones come last
+        if row == 6:
+            x[row] = -1.5
+            x[row, :cols // 3] = -INF                   # ties begin far from the row's start
+        x[row, kept] = values
+    check(s, top=20)
+    check(s, top=1)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("cols", [5, 2500])
 def test_padded_rows_have_gradient_zero(cols, dtype):
     """Whatever lies in them: their tokens are none, and the entropy's gradient is 0 or left out."""
