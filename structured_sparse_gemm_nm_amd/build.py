@@ -114,22 +114,34 @@ def check_sparse_operands(asm_path):
 
 
 # A matrix instruction's result is there a number of wait states after it; the
-# compiler fills them with s_nop. Where the result was stored to LDS in a block that
-# several others join, it has left them out, and LDS got what the registers held
-# before. The units below are read along every path for it.
-MATRIX_SOURCES = ("nm_lora.hip",)
-MATRIX_WAITS = 8                                   # of the 16x16 instructions
+# compiler fills them with s_nop. Where blocks join behind one (a result stored to LDS
+# in a block that several others join, a loop's last sum behind an early return) it has
+# left some out, and such a store got what the registers held before. Every unit that
+# holds matrix instructions is read along every path for it.
+MATRIX_SOURCES = SPARSE_SOURCES + ("nm_lora.hip",)
 
 
-def check_matrix_waits(asm_path, waits=MATRIX_WAITS):
-    """Instructions that use a 16x16 matrix instruction's result too early (empty list: sound)."""
+def _matrix_waits(op):
+    """Wait states between a matrix instruction and the first use of its result: two more than its passes of four
+    clocks take, 4 of them for the 16x16 instructions here and 8 for the 32x32 ones."""
+    return 12 if "_32x32x" in op else 8
+
+
+def check_matrix_waits(asm_path):
+    """Instructions that use a matrix instruction's result too early (empty list: sound). A matrix instruction that
+    goes on with the sum may follow at once; one that reads it as A, B or index may not."""
+    import functools
     import re
 
+    @functools.lru_cache(maxsize=None)
     def regs(t):
         out = set()
         for kind, lo, hi in re.findall(r"\b([av])\[(\d+):(\d+)\]", t):
             out |= {(kind, i) for i in range(int(lo), int(hi) + 1)}
         return out | {(kind, int(i)) for kind, i in re.findall(r"\b([av])(\d+)\b", t)}
+
+    def operands(rest):
+        return [o.strip() for o in rest.split(",")]
 
     code, labels, bad = [], {}, []
     for line in open(asm_path):
@@ -141,7 +153,8 @@ def check_matrix_waits(asm_path, waits=MATRIX_WAITS):
     for i, t in enumerate(code):
         if not t.startswith(("v_mfma", "v_smfmac")):
             continue
-        result, todo, seen = regs(t.split(",")[0]), [(i + 1, 0)], {}
+        waits, sums = _matrix_waits(t), operands(t.partition(" ")[2])[0]
+        result, todo, seen = regs(sums), [(i + 1, 0)], {}
         while todo:
             at, passed = todo.pop()
             if at >= len(code) or passed >= waits or seen.get(at, waits) <= passed:
@@ -149,7 +162,12 @@ def check_matrix_waits(asm_path, waits=MATRIX_WAITS):
             seen[at] = passed
             op, _, rest = code[at].partition(" ")
             if op.startswith(("v_mfma", "v_smfmac")):
-                if regs(rest.split(",")[0]) & result:   # a chain of sums: the next one's result counts
+                o = operands(rest)
+                addend, inputs = (o[3], o[1:3]) if op.startswith("v_mfma") else (o[0], o[1:4])
+                if any(regs(x) & result for x in inputs) or addend != sums and regs(addend) & result:
+                    bad.append("%s -> %s" % (t, code[at]))
+                    continue
+                if regs(o[0]) & result:                 # its own result counts from here on
                     continue
             elif regs(rest) & result:
                 bad.append("%s -> %s" % (t, code[at]))
@@ -166,7 +184,7 @@ def _compile(src):
     stem = os.path.splitext(src)[0]
     obj = os.path.join(BUILD, stem + ".o")
     cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
-    if src in SPARSE_SOURCES + MATRIX_SOURCES:
+    if src in MATRIX_SOURCES:
         cmd += ["-save-temps=obj"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines() if "packed-fp32-ops" not in l)

@@ -405,6 +405,13 @@ __global__ void __launch_bounds__(512) w4_kernel(W4Args A) {
 #pragma unroll
           for (int j = 0; j < NT; j++) y[r][j][e] = __builtin_fmaf(s1, (float)acc[r][j][e], y[r][j][e]);
         }
+      // The sums are taken here, in the block of the matrix instructions. Left to itself the compiler moves this
+      // behind the next tile's early return, and leaves out wait states on the way there; the build reads the
+      // units for it.
+#pragma unroll
+      for (int r = 0; r < R; r++)
+#pragma unroll
+        for (int j = 0; j < NT; j++) asm volatile("" : "+v"(y[r][j]));
     }
     ci++;
   };
