@@ -4,12 +4,13 @@
 gave, each token by the adapter that its index names: nm_lora. The product may be in 16
 bits (nm_w4_matvec, nm_spmm) or the int32 accumulators of an int8 one (``Rows``), the
 tokens in 16 bits or in the 8-bit codes that the product took. CompressedFeedForward
-takes them for its two projections. They serve: there is no backward pass.
+takes them for its two projections. They serve: there is no backward pass,
+nor a forward-mode derivative.
 """
 import torch
 
 from . import nm_lora, nm_lora_plan_init
-from .feed_forward import Rows, _DTYPE_NAMES, _Plans
+from .feed_forward import Rows, _DTYPE_NAMES, _Plans, refuse_tangents
 from .heads import _rows_on_16_bytes
 
 
@@ -48,6 +49,7 @@ class Adapters:
         tokens x out of the shared product, a 16-bit tensor or ``Rows``. Returns 16-bit rows: out, which may be base, or
         new ones."""
         base = base if isinstance(base, Rows) else Rows(base)
+        refuse_tangents(x, x_scale, *base, out)
         for t in (x, x_scale, *base, out):
             if torch.is_grad_enabled() and t is not None and t.requires_grad:
                 raise RuntimeError("adapters that are served have no backward pass: detach the operands, or call it "

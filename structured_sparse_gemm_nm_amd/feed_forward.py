@@ -23,11 +23,13 @@ token: nm_lora adds them to the product, from the same 8-bit codes.
 
 Features must be multiples of 16. Weights are prepared with torch; every call runs
 in the library's kernels and may be captured into a graph. There is no backward
-pass: operands that require a gradient are refused while gradients are recorded.
+pass: operands that require a gradient are refused while gradients are recorded, and
+those that carry a forward-mode tangent always.
 """
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import nm_compress, nm_plan_init, nm_prune, nm_rmsnorm, nm_rows_plan_init, nm_spmm, nm_swiglu, nm_w4_matvec, \
     nm_w4_pack, nm_w4_plan_init
@@ -74,6 +76,15 @@ class Rows(NamedTuple):
         """The values in fp32."""
         v = self.values.float()
         return v if self.row_scale is None else v * self.row_scale[:, None] * self.col_scale
+
+
+def refuse_tangents(*operands):
+    """The kernels read values alone: what a forward-mode tangent is for would be lost without a word. Tangents live
+    within a level, so that outside of one (0.1 us) no operand is looked at."""
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return
+    if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in operands):
+        raise RuntimeError("there is no forward-mode derivative: operands must not carry a tangent (unpack them first)")
 
 
 class _Weight:
@@ -152,9 +163,10 @@ class CompressedFeedForward:
             n, cols, op=op, dtype=_DTYPE_NAMES[self.dtype], x_dtype="i32" if acc else None, y_dtype="i8", eps=self.eps))
 
     def _check(self, x, residual):
-        """x is what a plan of the block can be made for, and no operand wants a gradient."""
+        """x is what a plan of the block can be made for, and no operand wants a gradient or carries a tangent."""
         v, row, col = x
         acc = v.dtype is torch.int32
+        refuse_tangents(v, row, col, residual)
         if not acc and v.dtype is not self.dtype:
             raise ValueError("x must be %s or int32 accumulators, got %s" % (self.dtype, v.dtype))
         if (row is not None) != acc or (col is not None) != acc:

@@ -4,7 +4,7 @@
 or ``Rows`` of int32 accumulators, and runs nm_head_norm_rope in one pass. From
 16-bit rows it is differentiable in the rows and in both gains
 (nm_head_norm_rope_backward), so it stands between a SemiStructuredSparseLinear and
-the attention in training too. A backward pass may be captured into a graph while no
+the attention in training too; operands with a forward-mode tangent are refused. A backward pass may be captured into a graph while no
 eager graph of the same leaves lives: torch ties their gradients to the stream of
 the first.
 """
@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import nm_head_norm_rope, nm_head_norm_rope_backward, nm_heads_plan_init
-from .feed_forward import Rows, _DTYPE_NAMES, _Plans
+from .feed_forward import Rows, _DTYPE_NAMES, _Plans, refuse_tangents
 
 _PLANS = _Plans()
 
@@ -59,6 +59,7 @@ class _NormRotate(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
+        refuse_tangents(dy)
         x, gamma_q, gamma_k, positions, table = ctx.saved_tensors
         plan, gains = ctx.plan, ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         dy = dy if dy.is_contiguous() and dy.data_ptr() % 16 == 0 else dy.clone(memory_format=torch.contiguous_format)
@@ -93,6 +94,7 @@ def norm_rotate(x, gamma_q, gamma_k, positions, table, heads, pairs="halves", ep
         raise ValueError("x must be (tokens x %d), got %s" % (sum(heads) * gamma_q.shape[0], tuple(v.shape)))
     if table is not None and table.dim() != 2:
         raise ValueError("table must be positions x rotary_dim")
+    refuse_tangents(*x, gamma_q, gamma_k, table)
     wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (v, gamma_q, gamma_k, *x[1:]))
     if torch.is_grad_enabled() and table is not None and table.requires_grad:
         raise RuntimeError("the table has no gradient")

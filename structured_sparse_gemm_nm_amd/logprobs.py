@@ -4,9 +4,9 @@
 accumulators that the head's product handed on, and runs nm_logprobs. From 16-bit or
 fp32 logits the log probabilities and the entropy are differentiable
 (nm_logprobs_backward): minus their mean is the loss that a language model is trained
-on, the entropy a term beside it. A backward pass may be captured into a graph while no
-eager graph of the same leaves lives: torch ties their gradients to the stream of
-the first.
+on, the entropy a term beside it; logits with a forward-mode tangent are refused. A
+backward pass may be captured into a graph while no eager graph of the same leaves
+lives: torch ties their gradients to the stream of the first.
 """
 from typing import NamedTuple, Optional
 
@@ -14,7 +14,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import nm_logprobs, nm_logprobs_backward, nm_logprobs_plan_init
-from .feed_forward import Rows, _Plans
+from .feed_forward import Rows, _Plans, refuse_tangents
 from .heads import _rows_on_16_bytes
 
 _NAMES = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int32: "i32"}
@@ -65,6 +65,7 @@ class _TokenLogprobs(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, g_logprob, g_entropy, *_):
+        refuse_tangents(g_logprob, g_entropy)
         x, tokens, stats, entropy = ctx.saved_tensors
         if g_logprob is None and g_entropy is None:
             return None, None, None, None, None
@@ -88,6 +89,7 @@ def token_logprobs(logits, tokens, temperature=1.0, top=0, entropy=False):
         raise ValueError("logits must be rows x vocabulary, got %s" % (tuple(x.shape),))
     if not temperature > 0:
         raise ValueError("temperature must be positive, got %r" % (temperature,))
+    refuse_tangents(*logits)
     wants = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in logits)
     if acc and wants:
         raise RuntimeError("accumulators have no gradient: call it under torch.no_grad()")
