@@ -80,7 +80,7 @@ class Rows(NamedTuple):
 
 def refuse_tangents(*operands):
     """The kernels read values alone: what a forward-mode tangent is for would be lost without a word. Tangents live
-    within a level, so that outside of one (0.1 us) no operand is looked at."""
+    within a level; outside of one no operand is looked at (0.2 us)."""
     if getattr(forward_ad, "_current_level", 0) < 0:
         return
     if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in operands):

@@ -27,13 +27,18 @@ def rotation_table(positions, rotary_dim, base=10000.0, device="cuda"):
     return torch.cat((angle.cos(), angle.sin()), 1).float()
 
 
+def _empty_rows(rows, cols, dtype, device):
+    """Rows that the library takes, on 16-byte boundaries, and no further apart."""
+    step = 16 // dtype.itemsize
+    return torch.empty((rows, (cols + step - 1) // step * step), dtype=dtype, device=device)[:, :cols]
+
+
 def _rows_on_16_bytes(t):
-    """t, or a copy of it in rows that the library takes: on 16-byte boundaries."""
+    """t, or a copy of it in rows that the library takes."""
     step = 16 // t.element_size()
     if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.stride(0) % step == 0 and t.data_ptr() % 16 == 0:
         return t
-    out = torch.empty((t.shape[0], (t.shape[1] + step - 1) // step * step), dtype=t.dtype, device=t.device)[:, :t.shape[1]]
-    return out.copy_(t)
+    return _empty_rows(*t.shape, t.dtype, t.device).copy_(t)
 
 
 def _plan(x, heads, dim, table, gamma, pairs, eps):

@@ -15,7 +15,7 @@ from torch.autograd.function import once_differentiable
 
 from . import nm_logprobs, nm_logprobs_backward, nm_logprobs_plan_init
 from .feed_forward import Rows, _Plans, refuse_tangents
-from .heads import _rows_on_16_bytes
+from .heads import _empty_rows, _rows_on_16_bytes
 
 _NAMES = {torch.float16: "f16", torch.bfloat16: "bf16", torch.float32: "f32", torch.int32: "i32"}
 _PLANS = _Plans()
@@ -32,8 +32,9 @@ class LogProbs(NamedTuple):
 
 def _plan(x, top, scale):
     key = (tuple(x.shape), x.stride(0), x.dtype, top, scale)
-    return _PLANS.get(key, lambda: nm_logprobs_plan_init(*x.shape, dtype=_NAMES[x.dtype], top=top, scale=scale,
-                                                         ldx=x.stride(0), ldg=x.stride(0)))
+    return _PLANS.get(key, lambda: nm_logprobs_plan_init(
+        *x.shape, dtype=_NAMES[x.dtype], top=top, scale=scale, ldx=x.stride(0),
+        ldg=_empty_rows(1, x.shape[1], x.dtype, "meta").stride(0)))
 
 
 def _forward(plan, x, tokens, entropy, stats, row_scale=None, col_scale=None):
@@ -69,7 +70,8 @@ class _TokenLogprobs(torch.autograd.Function):
         x, tokens, stats, entropy = ctx.saved_tensors
         if g_logprob is None and g_entropy is None:
             return None, None, None, None, None
-        dx = torch.empty_strided(x.shape, (x.stride(0), 1), dtype=x.dtype, device=x.device)
+        # in rows of its own: logits may be rows far apart in something much larger
+        dx = _empty_rows(*x.shape, x.dtype, x.device)
         g_logprob, g_entropy = (None if g is None else g.contiguous() for g in (g_logprob, g_entropy))
         nm_logprobs_backward(ctx.plan, x, tokens, stats, dx, g_logprob=g_logprob, g_entropy=g_entropy, entropy=entropy)
         return dx, None, None, None, None
