@@ -414,9 +414,10 @@ typedef struct {
   int32_t type_io;          /* y and the gains: NM_F16 or NM_BF16 */
   int32_t type_x;           /* type_io or NM_I32 */
   int64_t table_rows;       /* positions that the table holds, up to 2^31 */
-  int64_t ldx, ldy;         /* rows of x (and its gradient), of y (and its gradient) */
+  int64_t ldx, ldy;         /* rows of x, of y (and its gradient) */
   float eps;                /* finite and >= 0 */
   int32_t zero_rows;        /* rows of y that hold no token: 0, left as they were; 1, zeros */
+  int64_t ldg;              /* rows of x's gradient; 0: ldx */
 } nm_heads_problem_t;
 typedef struct nm_heads_plan* nm_heads_plan_t;
 nm_status_t nm_heads_plan_init(nm_heads_plan_t* plan, const nm_heads_problem_t* problem);
@@ -432,7 +433,7 @@ nm_status_t nm_head_norm_rope(nm_heads_plan_t plan, const void* dX, const float*
 
 /* The gradient, for x of type_io (NM_ERR_UNSUPPORTED for accumulators): from x, the
  * forward's other inputs and d_grad_y (rows x columns of type_io, ldy), d_grad_x (of
- * type_io, ldx; it may equal d_grad_y where ldx == ldy) and, where wanted, the gains'
+ * type_io, ldg; it may equal d_grad_y where ldg == ldy) and, where wanted, the gains'
  * gradients summed over tokens and heads (head_dim elements of type_io each;
  * d_grad_gamma_k exactly with d_grad_gamma_q where there are key heads). A row that
  * holds no token has gradient zero. The sums are taken in fp32, those of the blocks

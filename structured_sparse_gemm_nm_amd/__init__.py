@@ -61,7 +61,7 @@ class nm_heads_problem_t(ctypes.Structure):
                 ("heads_v", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
                 ("pairs", ctypes.c_int32), ("type_io", ctypes.c_int32), ("type_x", ctypes.c_int32),
                 ("table_rows", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("eps", ctypes.c_float),
-                ("zero_rows", ctypes.c_int32)]
+                ("zero_rows", ctypes.c_int32), ("ldg", ctypes.c_int64)]
 
 
 class nm_logprobs_problem_t(ctypes.Structure):
@@ -621,7 +621,7 @@ class HeadsPlan(_LayerPlan):
         table = (f32, (p.table_rows, p.rotary_dim), max(1, p.rotary_dim))
         common = gain, gain, (torch.int64, (p.rows,), None), table
         self._specs = (x_spec, (f32, shape[:1], None), (f32, shape[1:], None)) + common + (y_spec,)
-        self._back_specs = (x_spec,) + common + (y_spec, (self.io_dtype, shape, p.ldx), gain, gain,
+        self._back_specs = (x_spec,) + common + (y_spec, (self.io_dtype, shape, p.ldg or p.ldx), gain, gain,
                                                  (torch.uint8, (self.workspace_bytes,), None))
         self._norm_call = self._call("nm_head_norm_rope", 0, *self._specs)
         if x != "i32":
@@ -633,11 +633,11 @@ class HeadsPlan(_LayerPlan):
 
 
 def nm_heads_plan_init(rows, heads_q, heads_k, heads_v, head_dim, rotary_dim, pairs="halves", table_rows=0, dtype="f16",
-                       x_dtype=None, ldx=None, ldy=None, eps=1e-6, zero_rows=False):
+                       x_dtype=None, ldx=None, ldy=None, eps=1e-6, zero_rows=False, ldg=None):
     """Plan of the norms of query and key heads with their rotation (host only). pairs: "halves" (i, i + rotary_dim / 2)
     or "neighbours" (2i, 2i + 1); table_rows: the positions that the table of angles holds; dtype: the 16-bit type of y
     and the gains; x_dtype: dtype, or "i32" for an int8 product's accumulators; zero_rows: rows of y that hold no token
-    become zeros (else they stay as they were)."""
+    become zeros (else they stay as they were); ldg: rows of x's gradient (ldx unless given)."""
     if pairs not in PAIRS:
         raise ValueError("pairs must be one of %s, got %r" % (sorted(PAIRS), pairs))
     x_dtype = x_dtype or dtype
@@ -648,6 +648,7 @@ def nm_heads_plan_init(rows, heads_q, heads_k, heads_v, head_dim, rotary_dim, pa
     cols = max(1, (heads_q + heads_k + heads_v) * head_dim)
     p.ldx = ldx if ldx is not None else cols
     p.ldy = ldy if ldy is not None else cols
+    p.ldg = ldg or 0
     h = ctypes.c_void_p()
     _check(lib().nm_heads_plan_init(ctypes.byref(h), ctypes.byref(p)))
     return HeadsPlan(h, p, dtype, x_dtype)

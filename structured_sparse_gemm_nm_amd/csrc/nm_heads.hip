@@ -464,6 +464,7 @@ nm_status_t nm_heads_plan_init(nm_heads_plan_t* plan, const nm_heads_problem_t* 
   const int64_t cols = ((int64_t)p->heads_q + p->heads_k + p->heads_v) * p->head_dim;
   nm_status_t st = layer_rows(p->rows, cols, p->ldx, p->type_x == NM_I32 ? 4 : 2);
   if (st == NM_OK) st = layer_rows(p->rows, cols, p->ldy, 2);
+  if (st == NM_OK && p->ldg != 0) st = layer_rows(p->rows, cols, p->ldg, 2);
   if (st != NM_OK) return st;
   nm_heads_plan* pl = new (std::nothrow) nm_heads_plan();
   if (!pl) return layer_fail(NM_ERR_INVALID_ARG, "out of host memory");
@@ -538,7 +539,7 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
   a.y = (uint16_t*)d_grad_x;
   a.part = (float*)d_workspace;
   a.ldx = p.ldx;
-  a.ldy = p.ldx;
+  a.ldy = p.ldg ? p.ldg : p.ldx;
   a.lddy = p.ldy;
   hipStream_t s = (hipStream_t)stream;
   const bool f16 = p.type_io == NM_F16, halves = p.pairs == NM_PAIRS_HALVES;

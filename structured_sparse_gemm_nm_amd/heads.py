@@ -47,7 +47,7 @@ def _plan(x, heads, dim, table, gamma, pairs, eps):
     key = (x.shape[0], x.stride(0), heads, dim, rotary, table_rows, gamma.dtype, acc, pairs, eps)
     return _PLANS.get(key, lambda: nm_heads_plan_init(
         x.shape[0], *heads, dim, rotary, pairs=pairs, table_rows=table_rows, dtype=_DTYPE_NAMES[gamma.dtype],
-        x_dtype="i32" if acc else None, ldx=x.stride(0), eps=eps, zero_rows=True))
+        x_dtype="i32" if acc else None, ldx=x.stride(0), eps=eps, zero_rows=True, ldg=sum(heads) * dim))
 
 
 class _NormRotate(torch.autograd.Function):
@@ -68,7 +68,8 @@ class _NormRotate(torch.autograd.Function):
         x, gamma_q, gamma_k, positions, table = ctx.saved_tensors
         plan, gains = ctx.plan, ctx.needs_input_grad[1] or ctx.needs_input_grad[2]
         dy = dy if dy.is_contiguous() and dy.data_ptr() % 16 == 0 else dy.clone(memory_format=torch.contiguous_format)
-        dx = torch.empty_strided(x.shape, (x.stride(0), 1), dtype=x.dtype, device=x.device)
+        # in rows of its own: x may be rows far apart in something much larger
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dq = dk = workspace = None
         if gains:
             dq, dk = torch.empty_like(gamma_q), None if gamma_k is None else torch.empty_like(gamma_k)
