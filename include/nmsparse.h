@@ -505,6 +505,9 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
  *    (f16: after the token's largest was brought to 1 by a power of two), the second
  *    what that left over, so that it keeps 2^-16 (bf16) or 2^-22 (f16, of the token's
  *    largest) of its value. The rest is fp32, rounded once to type_y.
+ *  - An infinite or NaN A x keeps to its token, and its products with B are the formula's;
+ *    0 times an infinity is NaN, of ranks that are padded with zeros too. An infinity in B,
+ *    which both parts meet, may make NaN of its output.
  *  - A token's row depends on nothing but that token, its adapter and n.
  * There is no backward pass: adapters that are served are constants. */
 typedef struct {

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
         constexpr int JN = decltype(J)::n;
         typedef LoraStep<JN, XS> step_t;
         auto first_k = [&](int i) { return (((int64_t)blockIdx.x * A.loops + i) * parts + part) * LORA_KW; };
-        // what lies behind k is loaded from the row's last elements, and those that came before are dropped from A
+        // What lies behind k is loaded from the row's last elements, and those that came before are dropped from A, and
+        // from a 16-bit x too, whose infinities would make NaN of A's zeros.
         auto load = [&](step_t& S, int64_t k0, bool whole) {
           constexpr int E = X8 ? 16 : 8;          // elements of x in 16 bytes
 #pragma unroll
@@ -298,7 +299,10 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
               if (!whole) a = lora_drop(a, (int)min(at - from - 8 * h, (int64_t)8));
             }
 #pragma unroll
-            for (int j = 0; j < JN; j++) S.x[j][s] = lora_load(xr[j] + from * (X8 ? 1 : 2));
+            for (int j = 0; j < JN; j++) {
+              S.x[j][s] = lora_load(xr[j] + from * (X8 ? 1 : 2));
+              if (!X8 && !whole) S.x[j][s] = lora_drop(S.x[j][s], (int)min(at - from, (int64_t)E));
+            }
           }
           __builtin_amdgcn_sched_barrier(0);      // all are on their way
         };
@@ -317,6 +321,30 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
               }
               acc[j] = lora_mma<IO>(__builtin_bit_cast(v_t, S.a[s]), __builtin_bit_cast(v_t, b), acc[j]);
             }
+        };
+        // The same of 16 bytes of x a lane, for many tokens: a whole step of them, dropped, would not fit the registers
+        // (4096 tokens of k = m = 4096, 16-bit, 28.0 us with seven spilled, 27.4 so).
+        auto last_pieces = [&](int64_t k0) {
+          constexpr int E = X8 ? 16 : 8;
+#pragma unroll 1
+          for (int s = 0; s < XS && k0 + 4 * E * s < A.k; s++) {
+            const int64_t at = k0 + 4 * E * s + E * q, from = min(at, A.k - E);
+            const int drop = (int)min(at - from, (int64_t)E);
+            u32x4 a[E / 8], x[JN];
+#pragma unroll
+            for (int h = 0; h < E / 8; h++) a[h] = lora_load(ar + (from + 8 * h) * 2);
+#pragma unroll
+            for (int j = 0; j < JN; j++) x[j] = lora_load(xr[j] + from * (X8 ? 1 : 2));
+#pragma unroll
+            for (int h = 0; h < E / 8; h++) a[h] = lora_drop(a[h], drop - 8 * h);
+#pragma unroll
+            for (int j = 0; j < JN; j++)
+#pragma unroll
+              for (int h = 0; h < E / 8; h++) {
+                const u32x4 b = X8 ? lora_codes<IO>(x[j][2 * h], x[j][2 * h + 1]) : lora_drop(x[j], drop);
+                acc[j] = lora_mma<IO>(__builtin_bit_cast(v_t, a[h]), __builtin_bit_cast(v_t, b), acc[j]);
+              }
+          }
         };
         int steps = 0;                            // of the wave's, those that lie within k whole
         while (steps < A.loops && first_k(steps) + LORA_KW <= A.k) steps++;
@@ -337,8 +365,12 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
           multiply(S);
         }
         if (steps < A.loops && first_k(steps) < A.k) {
-          load(S, first_k(steps), false);
-          multiply(S);
+          if constexpr (NT > 1) {
+            last_pieces(first_k(steps));
+          } else {
+            load(S, first_k(steps), false);
+            multiply(S);
+          }
         }
       };
       if (16 * rt < A.rank) {
@@ -476,16 +508,15 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
               if (s + i < A.splits) v += w[i];
           }
           if (r >= A.rank || !cols.has(c0 + j)) v = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-          float up = 1.0f, fac = sa * xs;
-          if constexpr (IO == DT_F16) {
-            // the token's largest below 1: times 2^-x with x its exponent's distance; not for 0, infinities and NaN
-            float top = 0.0f;                     // a NaN is not among them; it stays in t
+          float up = 1.0f, fac = sa * xs, top = 0.0f;       // a NaN is not the largest; it stays in t
 #pragma unroll
-            for (int i = 0; i < 4; i++) top = fmaxf(top, __builtin_fabsf(v[i]));
+          for (int i = 0; i < 4; i++) top = fmaxf(top, __builtin_fabsf(v[i]));
+          if constexpr (IO == DT_F16) {
+            // the token's largest below 1: times 2^-x with x its exponent's distance; not for 0
 #pragma unroll
             for (int off = 1; off < PER; off *= 2) top = fmaxf(top, __shfl_xor(top, off));
             const int x = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 126;
-            if (x > -126 && x < 129) {
+            if (x > -126) {
               up = __builtin_ldexpf(1.0f, -min(x, 120));      // 2^-127 is none; 2^8 f16 still holds
               fac *= __builtin_ldexpf(1.0f, min(x, 120));
             }
@@ -497,6 +528,20 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
             const uint16_t ha = to_bits16<IO>(a), hb = to_bits16<IO>(b);
             hi[i] = (uint32_t)ha | (uint32_t)hb << 16;
             lo[i] = (uint32_t)to_bits16<IO>(a - from_bits16<IO>(ha)) | (uint32_t)to_bits16<IO>(b - from_bits16<IO>(hb)) << 16;
+          }
+          // Infinities have no second part (and decide what the token's others are next to them). A finite t that bf16
+          // rounds to one becomes the type's largest value and the rest.
+          if (!(top < (IO == DT_F16 ? INFINITY : 0x1.FEp127f))) {
+            lo[0] = lo[1] = 0;
+            if constexpr (IO == DT_BF16) {
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const int at = 16 * (i % 2);
+                if ((hi[i / 2] >> at & 0x7FFF) == 0x7F80 && __builtin_fabsf(v[i]) < INFINITY) hi[i / 2] -= 1u << at;
+                if (__builtin_fabsf(v[i]) < INFINITY)
+                  lo[i / 2] |= (uint32_t)to_bits16<IO>(v[i] - from_bits16<IO>((uint16_t)(hi[i / 2] >> at))) << at;
+              }
+            }
           }
           *(u32x2*)&ts[j][r] = u32x2{hi[0], hi[1]};
           *(u32x2*)&ts[j][RANKS + r] = u32x2{lo[0], lo[1]};
