@@ -356,7 +356,7 @@ __device__ __forceinline__ void lp_write_top(const LpArgs& A, int64_t row, const
 
 // What the alternatives of a row need in LDS.
 template <int W> struct LpLists {
-  uint64_t keys[W][LP_CAP];
+  alignas(16) uint64_t keys[W][LP_CAP];   // and lp_nth's floats, read four at a time
   int chunks[W][LP_CHUNKS / W];
   int counts[W];
   int tied;               // columns of the bound at the row's start

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs
   // 37 tokens of k = 11008 27.6 and 30.6; rank 16, 16 tokens of k = 4096 10.4 and 10.8, 4096 tokens 44.9 and 51.1.
   constexpr int WS = NT == 1 && SETS == 2 ? 8 : 4;
   constexpr int BQ = ACC ? 2 : 1;                         // pieces of 16 bytes a lane's outputs take of the base
-  __shared__ uint16_t ts[16 * NT][2 * RANKS + 8];         // both parts of t; 16 tokens lie on distinct banks
+  alignas(16) __shared__ uint16_t ts[16 * NT][2 * RANKS + 8];   // both parts of t, read in 16 bytes; 16 tokens lie on distinct banks
   __shared__ float factor[16 * NT];
   __shared__ int tokens[OWN ? 1 : LORA_WAVES][LORA_TILE];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, q = lane >> 4;
