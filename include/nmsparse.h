@@ -497,8 +497,8 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
  * for n tokens x (n x k; x_scale is 1 where x is of type_y). A holds the adapters one
  * after the other, rank rows of k each (adapters * rank rows, lda), B m rows of rank
  * each (adapters * m rows, rank elements apart); smaller ranks are padded with zeros.
- * base (n x m, ldc) is what the projection gave: of type_y, where it may be y itself,
- * or nm_spmm's int32 accumulators, whose value is base * row_scale * col_scale.
+ * base (n x m, ldc) is what the projection gave: of type_y, where it may be y itself
+ * (ldc == ldy), or nm_spmm's int32 accumulators, whose value is base * row_scale * col_scale.
  *  - A negative index names no adapter: y[j] = base[j] (a row that is its own base is
  *    not written). An index of `adapters` or more: the row is NaN.
  *  - A x is summed in fp32 and meets B as two 16-bit parts: the first rounded to type_y

@@ -497,6 +497,8 @@ nm_status_t nm_head_norm_rope(nm_heads_plan_t plan, const void* dX, const float*
   if (!dY) return layer_fail(NM_ERR_INVALID_ARG, "dY is NULL");
   if ((d_row_scale != nullptr) != acc || (d_col_scale != nullptr) != acc)
     return layer_fail(NM_ERR_INVALID_ARG, "d_row_scale and d_col_scale must be given exactly where x is int32");
+  if (dY == dX && (acc || (p.rows > 1 && p.ldx != p.ldy)))
+    return layer_fail(NM_ERR_INVALID_ARG, "dY may equal dX only where x is of type_io and ldx == ldy");
   HeadArgs a = head_args(p, d_gamma_q, d_gamma_k, d_positions, d_table);
   a.x = (const uint8_t*)dX;
   a.row_scale = d_row_scale;
@@ -533,13 +535,18 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
     return layer_fail(NM_ERR_INVALID_ARG, "d_grad_gamma_k must be given exactly with d_grad_gamma_q where there are key heads");
   if (p.rows && (!d_grad_y || !d_grad_x)) return layer_fail(NM_ERR_INVALID_ARG, "d_grad_y / d_grad_x is NULL");
   if (p.rows && gain && !d_workspace) return layer_fail(NM_ERR_INVALID_ARG, "the gains' gradients need a workspace");
+  const int64_t ldg = p.ldg ? p.ldg : p.ldx;
+  if (p.rows > 1 && d_grad_x == d_grad_y && ldg != p.ldy)
+    return layer_fail(NM_ERR_INVALID_ARG, "d_grad_x may equal d_grad_y only where ldg == ldy");
+  if (p.rows > 1 && d_grad_x == dX && ldg != p.ldx)
+    return layer_fail(NM_ERR_INVALID_ARG, "d_grad_x may not equal dX where ldg != ldx");
   HeadArgs a = head_args(p, d_gamma_q, d_gamma_k, d_positions, d_table);
   a.x = (const uint8_t*)dX;
   a.dy = (const uint16_t*)d_grad_y;
   a.y = (uint16_t*)d_grad_x;
   a.part = (float*)d_workspace;
   a.ldx = p.ldx;
-  a.ldy = p.ldg ? p.ldg : p.ldx;
+  a.ldy = ldg;
   a.lddy = p.ldy;
   hipStream_t s = (hipStream_t)stream;
   const bool f16 = p.type_io == NM_F16, halves = p.pairs == NM_PAIRS_HALVES;

@@ -862,6 +862,8 @@ nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const 
   if (!d_grad_logprob && !d_grad_entropy) return layer_fail(NM_ERR_INVALID_ARG, "no gradient is given");
   if (d_grad_logprob && !d_tokens) return layer_fail(NM_ERR_INVALID_ARG, "d_grad_logprob needs d_tokens");
   if (d_grad_entropy && !d_entropy) return layer_fail(NM_ERR_INVALID_ARG, "d_grad_entropy needs d_entropy");
+  if (d_grad_x == dX && p.rows > 1 && p.ldg != p.ldx)
+    return layer_fail(NM_ERR_INVALID_ARG, "d_grad_x may equal dX only where ldg == ldx");
   LpBackArgs a = {};
   a.x = (const uint8_t*)dX;
   a.tokens = d_tokens;

@@ -738,6 +738,8 @@ nm_status_t nm_lora(nm_lora_plan_t plan, const void* dX, const float* d_x_scale,
   const bool acc = p.type_base == NM_I32;
   if ((d_row_scale != nullptr) != acc || (d_col_scale != nullptr) != acc)
     return layer_fail(NM_ERR_INVALID_ARG, "d_row_scale and d_col_scale must be given exactly where the base is int32");
+  if (dY == d_base && (acc || (p.n > 1 && p.ldc != p.ldy)))
+    return layer_fail(NM_ERR_INVALID_ARG, "dY may be d_base only where the base is of type_y and ldc == ldy");
   LoraArgs a = {};
   a.x = (const uint8_t*)dX;
   a.x_scale = d_x_scale;
