@@ -486,8 +486,9 @@ nm_status_t nm_logprobs(nm_logprobs_plan_t plan, const void* dX, const float* d_
  * One of d_grad_logprob (with d_tokens) and d_grad_entropy (with d_entropy, the
  * forward's) may be NULL: that term is left out. A row whose token is none has no g, a
  * row of -infinity alone gradient 0, and so has a row whose g and h are 0 or left out,
- * whatever its logits (a padded row's may be NaN). d_stats comes from nm_logprobs on
- * the same x and scale. d_grad_x may equal dX where ldg == ldx. */
+ * whatever its logits (a padded row's may be NaN) and its token; one with a token of
+ * cols or more and another g is NaN. d_stats comes from nm_logprobs on the same x and
+ * scale. d_grad_x may equal dX where ldg == ldx. */
 nm_status_t nm_logprobs_backward(nm_logprobs_plan_t plan, const void* dX, const int64_t* d_tokens, const float* d_stats,
                                  const float* d_entropy, const float* d_grad_logprob, const float* d_grad_entropy,
                                  void* d_grad_x, void* stream);

@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(LP_THREADS) lp_backward_kernel(LpBackArgs A) {
   const int64_t token = A.tokens ? A.tokens[row] : -1;
   const float m = A.stats[2 * row], logs = A.stats[2 * row + 1];
   float g = A.g_logprob && token >= 0 ? A.g_logprob[row] : 0.0f;
-  if (A.g_logprob && token >= A.cols) g = NAN;
+  if (token >= A.cols && g != 0.0f) g = NAN;
   if (logs == INFINITY) g = 0.0f;                 // no weight in the row
   float h = 0.0f, H = 0.0f;
   if constexpr (ENT) { h = A.g_entropy[row]; H = A.entropy[row]; }
