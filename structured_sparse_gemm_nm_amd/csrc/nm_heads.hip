@@ -209,8 +209,11 @@ __global__ void __launch_bounds__(HEAD_THREADS) heads_kernel(HeadArgs A) {
 // heads, and keep their shares of dgamma in registers; the groups' shares are added
 // in LDS in their order and written out, and heads_gain_kernel adds the blocks'. Memory
 // bounds it: 8192 tokens of 48 heads of 128, 302 MB, 62.6 us, 4.8 TB/s (70 us where a round's
-// loads were asked for in the round itself). Rounds of 3 heads a group, which divide 48 heads
-// of 128 among 16 groups: the case takes 101.9 us, with 2 heads 111.2, with 4 105.5.
+// loads were asked for in the round itself). Rounds of 3 heads a group; what a round is short of
+// is loaded for nothing. Forward and backward of 8192 tokens with rounds of 2, 3 and 4, in us:
+// 48 heads of 128 113.6, 103.4 and 106.8; 40 of 128 103.9, 94.2 and 99.3; 24 of 256 110.6, 99.6
+// and 103.8; 48 of 80 96.6, 86.0 and 91.0; but 64 of 128 134.8, 142.2 and 134.4, 40 of 64 63.1,
+// 83.1 and 87.0.
 template <int IO, bool HALVES, int G, bool GAIN>
 __global__ void __launch_bounds__(HEAD_THREADS) heads_backward_kernel(HeadArgs A) {
   constexpr int U = 3;

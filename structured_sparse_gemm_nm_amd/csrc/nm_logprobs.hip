@@ -706,7 +706,9 @@ static dim3 lp_grid(int64_t blocks) {
 
 // Logits that the caches do not hold until they are read again (256 MB on this card) are read past them, and so is
 // their gradient written: 4096 x 131072 bf16 (1 GB) forward and backward 566 us without, 522 with loads and 509 with
-// stores past them; 2048 x 32768 accumulators (268 MB) 60 us without and 66 with.
+// stores past them; 2048 x 32768 accumulators (268 MB) 60 us without and 66 with. bf16 rows of 131072, forward and
+// backward, without and with: 512 MB 308 and 278, 640 MB 392 and 364; below the edge, which the accumulators set, 450 MB
+// 273 and 246, 384 MB 228 and 206, 275 MB 167 and 151.
 static bool lp_streams(int64_t rows, int64_t cols, int size) { return rows * cols * size >= (int64_t)1 << 29; }
 
 // Half the threads where that keeps the chunks' list: 32003 f16 logits with 5 alternatives 9.7 us, 10.3 with all; but 16

@@ -96,7 +96,9 @@ __device__ __forceinline__ int lora_named(const LoraArgs& A, int64_t tile0, int&
 // 4096, bf16, in runs 24.5 us without it and 27.9 with it, scattered 174 and 34.8. So it runs from
 // where scattered tokens gain about that: 256 tokens over 64 adapters 26.4 us without and 22.9
 // with, over 8 12.0 and 16.3; 1024 over 8 28.4 and 23.2, over 4 22.3 and 23.4; 4096 over 4 33.7
-// and 29.8, over 2 27.6 and 30.8; 128 over 64 15.1 and 18.5.
+// and 29.8, over 2 27.6 and 30.8; 128 over 64 15.1 and 18.5. It stays one block: k = m = 1024, 64
+// adapters, without it and with it, 65536 tokens scattered 690 and 159, in runs 89 and 127; 262144
+// tokens 2620 and 577, in runs 322 and 464.
 __global__ void __launch_bounds__(LORA_SORT_THREADS) lora_sort_kernel(LoraArgs A, intx2* order) {
   constexpr int T = LORA_SORT_THREADS, B = LORA_SORT_BINS / T, U = 4;
   __shared__ int bins[LORA_SORT_BINS];
@@ -250,7 +252,8 @@ template <int J, int XS> struct LoraStep { u32x4 a[4], x[J][XS]; };   // what LO
 // their order. The instruction's rows are ranks, its columns tokens.
 // Latency bounds it for few tokens (16 of them, k = 4096, rank 16: 4.6 us for 2 MB), loads for
 // more (37 tokens of 24 adapters of rank 64, k = 11008: 10.3 us for 27 MB, 2.6 TB/s: 285 blocks on
-// 256 CUs; 4096 tokens of int8 codes 8.2 us for 17 MB).
+// 256 CUs; 4096 tokens of int8 codes 8.2 us for 17 MB). More than 64 tokens of a 16-bit x spill 8
+// registers, which are not needed in the loop over k.
 template <int IO, bool X8, int NT, bool OWN>
 __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs A) {
   typedef typename LoraType<IO>::v v_t;
@@ -322,8 +325,8 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
               acc[j] = lora_mma<IO>(__builtin_bit_cast(v_t, S.a[s]), __builtin_bit_cast(v_t, b), acc[j]);
             }
         };
-        // The same of 16 bytes of x a lane, for many tokens: a whole step of them, dropped, would not fit the registers
-        // (4096 tokens of k = m = 4096, 16-bit, 28.0 us with seven spilled, 27.4 so).
+        // The same of 16 bytes of x a lane, for many tokens: a whole step of them, dropped, costs time
+        // (4096 tokens of k = m = 4096, 16-bit, no tail among them, 28.0 us beside 27.4).
         auto last_pieces = [&](int64_t k0) {
           constexpr int E = X8 ? 16 : 8;
 #pragma unroll 1
@@ -404,8 +407,11 @@ __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_inner_kernel(LoraArgs
 // SETS: chunks of eight ranks a lane takes; 0: up to 16 ranks, both parts in one instruction.
 // Memory bounds it for prompts: 4096 tokens to 6144 features beside accumulators, 151 MB, 33 us,
 // 4.6 TB/s (with 64 outputs a wave 40 us: half the waves); for few tokens latency, 3.4 us for one
-// and 6.4 for 16 tokens to 22016 features (13 MB). Seven of the 64 variants spill 4 to 23 registers,
-// ranks over 64 beside accumulators most: their loads are in flight together.
+// and 6.4 for 16 tokens to 22016 features (13 MB). Six of the 64 variants spill, all beside
+// accumulators, whose loads are in flight together: f16 4 registers for ranks 17 to 32 (17 to 64
+// tokens, many outputs), 6 and 23 for ranks over 64 (up to 64 tokens and more), bf16 4 for ranks
+// 33 to 64 (more than 64 tokens), 4 and 18 over 64. f16, rank 128: 37 tokens of k = 11008 31 us
+// with the inner product, 1024 tokens of k = m = 4096 42 us.
 template <int IO, bool ACC, int SETS, int NT, bool OWN, int FB>
 __global__ void __launch_bounds__(64 * LORA_WAVES, 4) lora_outer_kernel(LoraArgs A) {
   typedef typename LoraType<IO>::v v_t;
