@@ -452,7 +452,8 @@ nm_status_t nm_head_norm_rope_backward(nm_heads_plan_t plan, const void* dX, con
  * and the top largest logits' columns and log probabilities in their order, the
  * lower of two equal ones' columns first. A logit is the fp32 value of x (of
  * NM_I32: (x * row_scale) * col_scale, each product rounded to fp32); sums are
- * taken in fp32, against the row's largest logit.
+ * taken in fp32, against the row's largest logit, from which the others' distances
+ * have fp32's range too.
  *  - A negative token is none: its log probability is 0. A token of cols or more: NaN.
  *  - Logits of -infinity have probability 0 and no part in the entropy. A row of
  *    nothing else: log probabilities -infinity, entropy 0.
