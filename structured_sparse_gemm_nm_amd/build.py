@@ -122,8 +122,8 @@ MATRIX_SOURCES = SPARSE_SOURCES + ("nm_lora.hip",)
 
 
 def _matrix_waits(op):
-    """Wait states between a matrix instruction and the first use of its result: two more than its passes of four
-    clocks take, 4 of them for the 16x16 instructions here and 8 for the 32x32 ones."""
+    """Wait states between a matrix instruction and the first use of its result: four more than its passes, which are 4
+    for the 16x16 instructions here and 8 for the 32x32 ones (what the compiler leaves within a block)."""
     return 12 if "_32x32x" in op else 8
 
 
