@@ -26,6 +26,7 @@ in the library's kernels and may be captured into a graph. There is no backward
 pass: operands that require a gradient are refused while gradients are recorded, and
 those that carry a forward-mode tangent always.
 """
+import threading
 from typing import NamedTuple, Optional
 
 import torch
@@ -49,19 +50,28 @@ MOST_PLANS = 256
 
 
 class _Plans:
+    """Threads may share one: the Python forms of the operators keep theirs for the whole process."""
+
     def __init__(self):
-        self._kept = {}
+        self._kept, self._lock = {}, threading.RLock()
 
     def __len__(self):
         return len(self._kept)
 
+    def __reduce__(self):
+        return _Plans, ()                          # a copy makes plans of its own
+
     def get(self, key, make):
-        plan = self._kept.pop(key, None)
-        if plan is None:
-            plan = make()
-        self._kept[key] = plan                     # the last in the dictionary's order
-        if len(self._kept) > MOST_PLANS:
-            self._kept.pop(next(iter(self._kept)), None)
+        with self._lock:
+            plan = self._kept.pop(key, None)
+            if plan is not None:
+                self._kept[key] = plan             # the last in the dictionary's order
+                return plan
+        plan = make()
+        with self._lock:
+            plan = self._kept.setdefault(key, plan)        # another thread's may be there by now
+            while len(self._kept) > MOST_PLANS:
+                self._kept.pop(next(iter(self._kept)))
         return plan
 
 
